@@ -378,6 +378,128 @@ attn_status_t attn_decode_paged_score_mod(const void* q, const void* k_pages, co
                                           void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * The 8-bit KV cache (attn_cache_*_q8, attn_decode_*_q8).  (No counterpart on
+ * the pages: the serving-side form of the cache the decode reads.)
+ *
+ * A cached row (one token of one KV head, d values) is d e4m3 codes (one byte
+ * each) and one scale byte e; the row's values are code * 2^(e - 127).  Rows lie
+ * as in the bf16 caches:
+ *   k_cache, v_cache  [B, Hkv, Lk_max, d] codes, 16-byte aligned, and
+ *   k_exp, v_exp      [B, Hkv, Lk_max] scale bytes, or
+ *   k_pages, v_pages  [num_pages, Hkv, page_size, d] codes and
+ *   k_exp, v_exp      [num_pages, Hkv, page_size] scale bytes, found through
+ *                     block_table as in attn_decode_paged (same page sizes).
+ * The scale of a row x is the smallest e >= 1 with max_c |x_c| <= 448 * 2^(e - 127)
+ * (448 is the largest e4m3 value), and its codes are x_c * 2^(127 - e) rounded to
+ * the nearest e4m3 value, ties to even: |x_c - code_c * 2^(e-127)| is at most
+ * 2^-4 |x_c|, or 2^(e - 137) for values below the e4m3 normal range.  K and V have
+ * scales of their own.
+ */
+
+/*
+ * attn_cache_append_q8 — write the new tokens' K and V rows into an 8-bit cache.
+ *
+ * Sequence b gets n_b = new_lens[b] new rows (Ln when new_lens is NULL), which
+ * become the last n_b of its kv_lens[b] keys: row i goes to position
+ * kv_lens[b] - n_b + i.  kv_lens thus counts the new keys already, as the
+ * decode that follows wants it.  Nothing else in the cache is touched.
+ * Infinities are stored as +-448 times the scale the row's finite values give,
+ * NaN as NaN.
+ *
+ * Arguments
+ *   k, v     [B, Hkv, Ln, d] bf16, read (rows at or past new_lens[b] are not)
+ *   k_cache, v_cache, k_exp, v_exp  the cache above, written
+ *   kv_lens  [B] int32 DEVICE array, each in [n_b, Lk_max]
+ *   new_lens [B] int32 DEVICE array, each in [0, Ln], or NULL
+ *   B, Hkv, Ln, Lk_max >= 1, B * Hkv * Ln < 2^31; d in {64, 128}
+ * A sequence whose kv_lens or new_lens entry is out of range is skipped and
+ * flags the device error word (ATTN_ERR_INVALID_ARG).
+ * Errors: INVALID_ARG / UNSUPPORTED before any launch; CUDA on launch failure.
+ */
+attn_status_t attn_cache_append_q8(const void* k, const void* v, void* k_cache, void* v_cache,
+                                   uint8_t* k_exp, uint8_t* v_exp, const int32_t* kv_lens,
+                                   const int32_t* new_lens, int B, int Hkv, int Ln, int Lk_max,
+                                   int d, void* stream);
+
+/*
+ * attn_cache_append_paged_q8 — attn_cache_append_q8 into pages.  Lk_max is
+ * pages_per_seq * page_size; a new row whose page id is outside [0, num_pages)
+ * is not written and flags the device error word (ATTN_ERR_INVALID_ARG).
+ * Sequences may share pages (a common prefix), but no two new rows may go to
+ * the same place.
+ */
+attn_status_t attn_cache_append_paged_q8(const void* k, const void* v, void* k_pages,
+                                         void* v_pages, uint8_t* k_exp, uint8_t* v_exp,
+                                         const int32_t* block_table, const int32_t* kv_lens,
+                                         const int32_t* new_lens, int B, int Hkv, int Ln,
+                                         int page_size, int pages_per_seq, int num_pages, int d,
+                                         void* stream);
+
+/*
+ * attn_cache_read_q8 — the first kv_lens[b] rows of every sequence and head of an
+ * 8-bit cache as bf16 (for a prefill over the cached context, or to inspect it).
+ *
+ * Arguments
+ *   k_cache, v_cache, k_exp, v_exp  the cache above, read below kv_lens[b]
+ *   kv_lens  [B] int32 DEVICE array, each in [0, Lk_max]; a sequence whose entry
+ *            is out of range is skipped and flags the device error word
+ *   k, v     [B, Hkv, Lk_max, d] bf16, rows below kv_lens[b] written (the exact
+ *            values code * 2^(e - 127), which bf16 holds in its normal range); the
+ *            other rows are left as they were
+ *   B * Hkv * Lk_max < 2^31; the rest as for attn_cache_append_q8
+ * Errors: INVALID_ARG / UNSUPPORTED before any launch; CUDA on launch failure.
+ */
+attn_status_t attn_cache_read_q8(const void* k_cache, const void* v_cache, const uint8_t* k_exp,
+                                 const uint8_t* v_exp, const int32_t* kv_lens, void* k, void* v,
+                                 int B, int Hkv, int Lk_max, int d, void* stream);
+
+/*
+ * attn_cache_read_paged_q8 — attn_cache_read_q8 from pages, with Lk_max =
+ * pages_per_seq * page_size in the outputs' shape; rows of a page id outside
+ * [0, num_pages) read as zeros and flag the device error word.
+ */
+attn_status_t attn_cache_read_paged_q8(const void* k_pages, const void* v_pages,
+                                       const uint8_t* k_exp, const uint8_t* v_exp,
+                                       const int32_t* block_table, const int32_t* kv_lens,
+                                       void* k, void* v, int B, int Hkv, int page_size,
+                                       int pages_per_seq, int num_pages, int d, void* stream);
+
+/*
+ * attn_decode_splitkv_q8 — attn_decode_splitkv over an 8-bit cache.
+ *
+ * Defines O and LSE of attn_decode_splitkv for the values the cache stands for:
+ *   S_ij = scale * 2^(k_exp_j - 127) * <Q_i, kc_j>,  j in [0, kv_lens[b]),
+ *   O_i = sum_j softmax_j(S_ij) 2^(v_exp_j - 127) vc_j,  LSE_i = log sum_j exp(S_ij).
+ * The codes go to the tensor cores as exact f16 values; scores and sums are
+ * fp32.  Codes and scale bytes at or past kv_lens[b] may hold anything.  A
+ * sequence with kv_lens[b] = 0 gets O = 0 and LSE = -inf.
+ *
+ * Arguments
+ *   q, o, lse, kv_lens, B, Hq, Hkv, Lq, Lk_max, d, scale, num_splits, workspace,
+ *   ws_bytes  as attn_decode_splitkv (the same split plan and workspace size)
+ *   k_cache, v_cache, k_exp, v_exp  the cache above, read below kv_lens[b]
+ * Errors: as attn_decode_splitkv.
+ */
+attn_status_t attn_decode_splitkv_q8(const void* q, const void* k_cache, const void* v_cache,
+                                     const uint8_t* k_exp, const uint8_t* v_exp, void* o,
+                                     float* lse, const int32_t* kv_lens, int B, int Hq, int Hkv,
+                                     int Lq, int Lk_max, int d, float scale, int num_splits,
+                                     void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * attn_decode_paged_q8 — attn_decode_splitkv_q8 over pages; arguments and errors
+ * as attn_decode_paged.  Block-table entries past a sequence's last page are
+ * never read.
+ */
+attn_status_t attn_decode_paged_q8(const void* q, const void* k_pages, const void* v_pages,
+                                   const uint8_t* k_exp, const uint8_t* v_exp,
+                                   const int32_t* block_table, void* o, float* lse,
+                                   const int32_t* kv_lens, int B, int Hq, int Hkv, int Lq,
+                                   int page_size, int pages_per_seq, int num_pages, int d,
+                                   float scale, int num_splits, void* workspace, size_t ws_bytes,
+                                   void* stream);
+
+/*
  * attn_decode_splitkv_noalloc — attn_decode_splitkv for callers that cannot
  * allocate device memory.  (No counterpart on the pages: this is a library
  * convenience, not part of the method.)

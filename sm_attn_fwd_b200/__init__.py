@@ -9,6 +9,9 @@ Entry points (same names as the C ABI):
   attn_fwd(q, k, v, ...)                 -> (o, lse)
   attn_fwd_host(q, k, v, ...)            -> (o, lse)   host tensors in and out
   attn_decode_splitkv(q, k, v, kv_lens, ...) -> (o, lse)
+  attn_cache_append_q8(k, v, k_cache, v_cache, k_exp, v_exp, kv_lens, ...)   8-bit cache, in place
+  attn_cache_read_q8(k_cache, v_cache, k_exp, v_exp, kv_lens, ...) -> (k, v)
+  attn_decode_splitkv_q8(q, k_cache, v_cache, k_exp, v_exp, kv_lens, ...) -> (o, lse)
   attn_decode_num_splits(...), attn_decode_workspace_size(...)
   attn_get_device_error(stream=None)     -> (status, raw_bits)
   attn_status_string(status)             -> str
@@ -32,6 +35,8 @@ __all__ = [
     "attn_decode_num_splits", "SCORE_MOD_NONE", "SCORE_MOD_ALIBI", "SCORE_MOD_REL_BIAS",
     "attn_decode_workspace_size", "attn_decode_paged", "attn_decode_splitkv_noalloc",
     "attn_decode_splitkv_score_mod", "attn_decode_paged_score_mod",
+    "attn_cache_append_q8", "attn_cache_append_paged_q8", "attn_cache_read_q8",
+    "attn_cache_read_paged_q8", "attn_decode_splitkv_q8", "attn_decode_paged_q8",
     "attn_get_device_error", "attn_selftest_wait_timeout", "attn_status_string",
     "EXPORTED_SYMBOLS",
 ]
@@ -58,6 +63,8 @@ EXPORTED_SYMBOLS = (
     "attn_decode_num_splits", "attn_decode_workspace_size",
     "attn_decode_splitkv", "attn_decode_paged", "attn_decode_splitkv_noalloc",
     "attn_decode_splitkv_score_mod", "attn_decode_paged_score_mod",
+    "attn_cache_append_q8", "attn_cache_append_paged_q8", "attn_cache_read_q8",
+    "attn_cache_read_paged_q8", "attn_decode_splitkv_q8", "attn_decode_paged_q8",
     "attn_get_device_error", "attn_selftest_wait_timeout", "attn_status_string",
 )
 
@@ -131,6 +138,18 @@ def load_library():
         lib.attn_decode_splitkv_noalloc.argtypes = [P, P, P, P, P, P, i32, i32, i32, i32, i32,
                                                     i32, f32, i32, P]
         lib.attn_decode_splitkv_noalloc.restype = i32
+        lib.attn_cache_append_q8.argtypes = [P] * 8 + [i32] * 5 + [P]
+        lib.attn_cache_append_q8.restype = i32
+        lib.attn_cache_append_paged_q8.argtypes = [P] * 9 + [i32] * 7 + [P]
+        lib.attn_cache_append_paged_q8.restype = i32
+        lib.attn_cache_read_q8.argtypes = [P] * 7 + [i32] * 4 + [P]
+        lib.attn_cache_read_q8.restype = i32
+        lib.attn_cache_read_paged_q8.argtypes = [P] * 8 + [i32] * 6 + [P]
+        lib.attn_cache_read_paged_q8.restype = i32
+        lib.attn_decode_splitkv_q8.argtypes = [P] * 8 + [i32] * 6 + [f32, i32, P, sz, P]
+        lib.attn_decode_splitkv_q8.restype = i32
+        lib.attn_decode_paged_q8.argtypes = [P] * 9 + [i32] * 8 + [f32, i32, P, sz, P]
+        lib.attn_decode_paged_q8.restype = i32
         lib.attn_get_device_error.argtypes = [P, ctypes.POINTER(ctypes.c_int)]
         lib.attn_get_device_error.restype = i32
         lib.attn_selftest_wait_timeout.argtypes = [P]
@@ -540,6 +559,202 @@ def attn_decode_splitkv_noalloc(q, k_cache, v_cache, kv_lens, *, scale=None, num
         Lq, Lk_max, d, float(scale), int(num_splits), _stream_handle(stream, q.device))
     if st != ATTN_OK:
         raise AttnError(st, "attn_decode_splitkv_noalloc")
+    return o, lse
+
+
+def _check(name, t, dtype, shape, device):
+    """t must be a contiguous CUDA tensor of this type and shape on ``device``."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _on(device):
+    """The library launches on the current device: make it the tensors' device."""
+    return torch.cuda.device(device)
+
+
+def _cache_shape(k_cache, block_table):
+    """(batch or None, Hkv, longest sequence, d, page_size, pages_per_seq, num_pages) of an
+    8-bit cache: contiguous when block_table is None, else pages."""
+    if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda:
+        raise ValueError("k_cache must be a CUDA tensor")
+    if k_cache.dim() != 4:
+        raise ValueError("the cache must have 4 dimensions: [B, Hkv, Lk_max, d], or "
+                         "[num_pages, Hkv, page_size, d] for pages")
+    n, Hkv, rows, d = k_cache.shape
+    if block_table is None:
+        return n, Hkv, rows, d, 0, 0, 0
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be an int32 CUDA tensor [B, pages_per_seq]")
+    return block_table.shape[0], Hkv, rows * block_table.shape[1], d, rows, block_table.shape[1], n
+
+
+def _check_q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, B):
+    dev = k_cache.device
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check(name, t, torch.float8_e4m3fn, k_cache.shape, dev)
+    for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
+        _check(name, t, torch.uint8, k_cache.shape[:3], dev)
+    if block_table is not None:
+        _check("block_table", block_table, torch.int32, block_table.shape, dev)
+    _check("kv_lens", kv_lens, torch.int32, (B,), dev)
+
+
+def attn_cache_append_q8(k, v, k_cache, v_cache, k_exp, v_exp, kv_lens, *, new_lens=None,
+                         stream=None):
+    """Write new tokens' K and V rows into an 8-bit cache, in place (see
+    ``attn_cache_append_q8`` in include/attn.h).
+
+    k, v: [B, Hkv, Ln, d] bf16; k_cache, v_cache: [B, Hkv, Lk_max, d]
+    torch.float8_e4m3fn; k_exp, v_exp: [B, Hkv, Lk_max] uint8 scale bytes (a row's
+    values are code * 2^(byte - 127)); kv_lens: [B] int32, the lengths with the new
+    tokens; new_lens: [B] int32, how many of the Ln rows each sequence gets (all
+    when not given).
+    """
+    _cache_append(k, v, k_cache, v_cache, k_exp, v_exp, None, kv_lens, new_lens, stream)
+
+
+def attn_cache_append_paged_q8(k, v, k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, *,
+                               new_lens=None, stream=None):
+    """attn_cache_append_q8 into pages (see ``attn_cache_append_paged_q8`` in
+    include/attn.h): k_pages, v_pages [num_pages, Hkv, page_size, d], k_exp, v_exp
+    [num_pages, Hkv, page_size], block_table [B, pages_per_seq] int32."""
+    if block_table is None:
+        raise ValueError("block_table must be an int32 CUDA tensor [B, pages_per_seq]")
+    _cache_append(k, v, k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, new_lens, stream)
+
+
+def _cache_append(k, v, k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, new_lens, stream):
+    B, Hkv, Lk, d, page, per_seq, n_pages = _cache_shape(k_cache, block_table)
+    _check_q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, B)
+    dev = k_cache.device
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be a [B, Hkv, Ln, d] CUDA tensor")
+    Ln = k.shape[2]
+    for name, t in (("k", k), ("v", v)):
+        _check(name, t, torch.bfloat16, (B, Hkv, Ln, d), dev)
+    if new_lens is not None:
+        _check("new_lens", new_lens, torch.int32, (B,), dev)
+    head = (_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(k_exp), _ptr(v_exp))
+    with _on(dev):
+        if block_table is None:
+            name = "attn_cache_append_q8"
+            st = load_library().attn_cache_append_q8(
+                *head, _ptr(kv_lens), _ptr(new_lens), B, Hkv, Ln, Lk, d,
+                _stream_handle(stream, dev))
+        else:
+            name = "attn_cache_append_paged_q8"
+            st = load_library().attn_cache_append_paged_q8(
+                *head, _ptr(block_table), _ptr(kv_lens), _ptr(new_lens), B, Hkv, Ln, page, per_seq,
+                n_pages, d, _stream_handle(stream, dev))
+    if st != ATTN_OK:
+        raise AttnError(st, name)
+
+
+def attn_cache_read_q8(k_cache, v_cache, k_exp, v_exp, kv_lens, *, k=None, v=None, stream=None):
+    """The first kv_lens[b] rows of an 8-bit cache as bf16 (see ``attn_cache_read_q8``
+    in include/attn.h).  Returns (k, v) [B, Hkv, Lk_max, d] bf16; rows at or past
+    kv_lens[b] are left as they are (undefined in tensors allocated here)."""
+    return _cache_read(k_cache, v_cache, k_exp, v_exp, None, kv_lens, k, v, stream)
+
+
+def attn_cache_read_paged_q8(k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, *, k=None,
+                             v=None, stream=None):
+    """attn_cache_read_q8 from pages (see ``attn_cache_read_paged_q8`` in
+    include/attn.h); Lk_max is pages_per_seq * page_size."""
+    if block_table is None:
+        raise ValueError("block_table must be an int32 CUDA tensor [B, pages_per_seq]")
+    return _cache_read(k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, k, v, stream)
+
+
+def _cache_read(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, k, v, stream):
+    B, Hkv, Lk, d, page, per_seq, n_pages = _cache_shape(k_cache, block_table)
+    _check_q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, B)
+    dev = k_cache.device
+    shape = (B, Hkv, Lk, d)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+    for name, t in (("k", k), ("v", v)):
+        _check(name, t, torch.bfloat16, shape, dev)
+    head = (_ptr(k_cache), _ptr(v_cache), _ptr(k_exp), _ptr(v_exp))
+    with _on(dev):
+        if block_table is None:
+            name = "attn_cache_read_q8"
+            st = load_library().attn_cache_read_q8(
+                *head, _ptr(kv_lens), _ptr(k), _ptr(v), B, Hkv, Lk, d, _stream_handle(stream, dev))
+        else:
+            name = "attn_cache_read_paged_q8"
+            st = load_library().attn_cache_read_paged_q8(
+                *head, _ptr(block_table), _ptr(kv_lens), _ptr(k), _ptr(v), B, Hkv, page, per_seq,
+                n_pages, d, _stream_handle(stream, dev))
+    if st != ATTN_OK:
+        raise AttnError(st, name)
+    return k, v
+
+
+def attn_decode_splitkv_q8(q, k_cache, v_cache, k_exp, v_exp, kv_lens, *, scale=None,
+                           num_splits=0, workspace=None, o=None, lse=None, stream=None):
+    """Split-KV decode over an 8-bit cache (see ``attn_decode_splitkv_q8`` in
+    include/attn.h).
+
+    q: [B, Hq, Lq, d] bf16; the cache as for ``attn_cache_append_q8``; kv_lens: [B]
+    int32.  ``workspace`` (uint8, attn_decode_workspace_size bytes) is allocated here
+    when not given.  Returns (o, lse).
+    """
+    return _decode_q8(q, k_cache, v_cache, k_exp, v_exp, None, kv_lens, scale, num_splits,
+                      workspace, o, lse, stream)
+
+
+def attn_decode_paged_q8(q, k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, *, scale=None,
+                         num_splits=0, workspace=None, o=None, lse=None, stream=None):
+    """attn_decode_splitkv_q8 over pages (see ``attn_decode_paged_q8`` in
+    include/attn.h); the cache as for ``attn_cache_append_paged_q8``."""
+    if block_table is None:
+        raise ValueError("block_table must be an int32 CUDA tensor [B, pages_per_seq]")
+    return _decode_q8(q, k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, scale, num_splits,
+                      workspace, o, lse, stream)
+
+
+def _decode_q8(q, k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, scale, num_splits,
+               workspace, o, lse, stream):
+    B, Hkv, Lk, d, page, per_seq, n_pages = _cache_shape(k_cache, block_table)
+    _check_q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, B)
+    dev = k_cache.device
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a [B, Hq, Lq, d] CUDA tensor")
+    _, Hq, Lq, _ = q.shape
+    _check("q", q, torch.bfloat16, (B, Hq, Lq, d), dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    o = torch.empty_like(q) if o is None else o
+    _check("o", o, torch.bfloat16, q.shape, dev)
+    if lse is None:
+        lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=dev)
+    _check("lse", lse, torch.float32, (B, Hq, Lq), dev)
+    head = (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_exp), _ptr(v_exp))
+    lib = load_library()
+    with _on(dev):
+        if workspace is None:
+            need = attn_decode_workspace_size(B, Hq, Hkv, Lq, Lk, d, num_splits)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        tail = (float(scale), int(num_splits), _ptr(workspace),
+                workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
+        if block_table is None:
+            name = "attn_decode_splitkv_q8"
+            st = lib.attn_decode_splitkv_q8(*head, _ptr(o), _ptr(lse), _ptr(kv_lens), B, Hq, Hkv,
+                                            Lq, Lk, d, *tail)
+        else:
+            name = "attn_decode_paged_q8"
+            st = lib.attn_decode_paged_q8(*head, _ptr(block_table), _ptr(o), _ptr(lse),
+                                          _ptr(kv_lens), B, Hq, Hkv, Lq, page, per_seq, n_pages, d,
+                                          *tail)
+    if st != ATTN_OK:
+        raise AttnError(st, name)
     return o, lse
 
 

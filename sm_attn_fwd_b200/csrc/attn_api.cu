@@ -14,6 +14,7 @@
 #include "attn.h"
 #include "attn_bwd_params.h"
 #include "attn_params.h"
+#include "cache_q8_params.h"
 #include "host_once.h"
 
 namespace attn {
@@ -35,6 +36,14 @@ cudaError_t launch_selftest_wait(cudaStream_t stream);
 template <int D>
 cudaError_t launch_short(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
                          const FwdParams&, int, cudaStream_t);
+template <int D>
+cudaError_t launch_cache_append(const CacheParams&, cudaStream_t);
+template <int D>
+cudaError_t launch_cache_read(const CacheParams&, cudaStream_t);
+template <int D>
+cudaError_t launch_decode_q8(const CUtensorMap&, const CUtensorMap&, const DecodeQ8Params&,
+                             cudaStream_t);
+int decode_q8_box_rows(int page_size);
 }  // namespace attn
 
 namespace {
@@ -188,6 +197,25 @@ bool encode_bf16_packed(CUtensorMap* map, const void* base, int d, int H, int to
                     gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+  });
+}
+
+// 8-bit codes {d, rows, planes}: boxes of a whole row (d = 64 or 128 bytes) by
+// box_rows rows, swizzled over the row's width; out-of-range rows read as zero.
+bool encode_codes(CUtensorMap* map, const void* base, const uint64_t* dims, int box_rows) {
+  TmapKey key{base, {dims[0], dims[1], dims[2]}, 3, box_rows, 3};
+  return cached_encode(map, key, [&](CUtensorMap* out) {
+    auto fn = get_encode_fn();
+    if (!fn) return false;
+    cuuint64_t gdim[3] = {dims[0], dims[1], dims[2]};
+    cuuint64_t gstride[2] = {dims[0], dims[0] * dims[1]};
+    cuuint32_t box[3] = {(cuuint32_t)dims[0], (cuuint32_t)box_rows, 1};
+    cuuint32_t estride[3] = {1, 1, 1};
+    CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3u, const_cast<void*>(base), gdim, gstride,
+                    box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    dims[0] == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
   });
 }
@@ -925,24 +953,35 @@ attn_status_t attn_decode_splitkv_score_mod(const void* q, const void* k_cache,
 
 namespace {
 
+// Checks a paged cache's arguments; fills *pg and *lk, the longest a sequence can be.
+attn_status_t parse_paged(const int32_t* block_table, int Hkv, int page_size, int pages_per_seq,
+                          int num_pages, PagedKv* pg, int* lk) {
+  if (!block_table || !aligned(block_table, 4)) return ATTN_ERR_INVALID_ARG;
+  if (page_size < 16 || page_size > (1 << 16) || (page_size & (page_size - 1)) != 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (pages_per_seq < 1 || num_pages < 1 || Hkv < 1) return ATTN_ERR_INVALID_ARG;
+  const long long n = (long long)pages_per_seq * page_size;
+  if (n > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)num_pages * Hkv > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  pg->block_table = block_table;
+  pg->page_size = page_size;
+  pg->pages_per_seq = pages_per_seq;
+  pg->num_pages = num_pages;
+  *lk = (int)n;
+  return ATTN_OK;
+}
+
 attn_status_t paged_impl(const void* q, const void* k_pages, const void* v_pages,
                          const int32_t* block_table, void* o, float* lse, const int32_t* kv_lens,
                          int B, int Hq, int Hkv, int Lq, int page_size, int pages_per_seq,
                          int num_pages, int d, float scale, int num_splits, void* workspace,
                          size_t ws_bytes, void* stream, const ScoreMod& sm) {
-  if (!block_table || !aligned(block_table, 4)) return ATTN_ERR_INVALID_ARG;
-  if (page_size < 16 || page_size > (1 << 16) || (page_size & (page_size - 1)) != 0)
-    return ATTN_ERR_INVALID_ARG;
-  if (pages_per_seq < 1 || num_pages < 1 || Hkv < 1) return ATTN_ERR_INVALID_ARG;
-  const long long lk = (long long)pages_per_seq * page_size;
-  if (lk > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
-  if ((long long)num_pages * Hkv > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   PagedKv pg;
-  pg.block_table = block_table;
-  pg.page_size = page_size;
-  pg.pages_per_seq = pages_per_seq;
-  pg.num_pages = num_pages;
-  return decode_impl(q, k_pages, v_pages, o, lse, kv_lens, B, Hq, Hkv, Lq, (int)lk, d, scale,
+  int lk = 0;
+  const attn_status_t st =
+      parse_paged(block_table, Hkv, page_size, pages_per_seq, num_pages, &pg, &lk);
+  if (st != ATTN_OK) return st;
+  return decode_impl(q, k_pages, v_pages, o, lse, kv_lens, B, Hq, Hkv, Lq, lk, d, scale,
                      num_splits, workspace, ws_bytes, stream, pg, sm);
 }
 
@@ -975,6 +1014,235 @@ attn_status_t attn_decode_paged_score_mod(const void* q, const void* k_pages, co
                     pages_per_seq, num_pages, d, scale, num_splits, workspace, ws_bytes, stream,
                     sm);
 }
+
+}  // extern "C"
+
+// ------------------------------------------------------- 8-bit KV cache
+namespace {
+
+int log2_of(int pow2) {
+  int s = 0;
+  while ((1 << s) < pow2) ++s;
+  return s;
+}
+
+// Arguments shared by append and read-back.
+attn_status_t cache_params(const void* k_codes, const void* v_codes, const uint8_t* k_exp,
+                           const uint8_t* v_exp, const int32_t* kv_lens, int B, int Hkv, int Lk,
+                           int d, const PagedKv& pg, attn::CacheParams* p) {
+  if (!k_codes || !v_codes || !k_exp || !v_exp || !kv_lens) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(kv_lens, 4))
+    return ATTN_ERR_INVALID_ARG;
+  if (B < 1 || Hkv < 1 || Lk < 1) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  std::memset(p, 0, sizeof *p);
+  p->k_codes = const_cast<void*>(k_codes);
+  p->v_codes = const_cast<void*>(v_codes);
+  p->k_exp = const_cast<uint8_t*>(k_exp);
+  p->v_exp = const_cast<uint8_t*>(v_exp);
+  p->kv_lens = kv_lens;
+  p->B = B;
+  p->Hkv = Hkv;
+  p->Lk = Lk;
+  p->block_table = pg.block_table;
+  p->page_shift = pg.block_table ? log2_of(pg.page_size) : 0;
+  p->pages_per_seq = pg.pages_per_seq;
+  p->num_pages = pg.num_pages;
+  return ATTN_OK;
+}
+
+attn_status_t append_impl(const void* k, const void* v, void* k_codes, void* v_codes,
+                          uint8_t* k_exp, uint8_t* v_exp, const int32_t* kv_lens,
+                          const int32_t* new_lens, int B, int Hkv, int Ln, int Lk, int d,
+                          const PagedKv& pg, void* stream) {
+  attn::CacheParams p;
+  const attn_status_t vs =
+      cache_params(k_codes, v_codes, k_exp, v_exp, kv_lens, B, Hkv, Lk, d, pg, &p);
+  if (vs != ATTN_OK) return vs;
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return ATTN_ERR_INVALID_ARG;
+  if (Ln < 1 || (new_lens && !aligned(new_lens, 4))) return ATTN_ERR_INVALID_ARG;
+  if ((long long)B * Hkv > 0x7fffffffLL / Ln) return ATTN_ERR_UNSUPPORTED;
+  p.k_in = k;
+  p.v_in = v;
+  p.new_lens = new_lens;
+  p.Ln = Ln;
+  p.err = error_word_for_current_device();
+  if (!p.err) return ATTN_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      d == 64 ? attn::launch_cache_append<64>(p, st) : attn::launch_cache_append<128>(p, st);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status_t read_impl(const void* k_codes, const void* v_codes, const uint8_t* k_exp,
+                        const uint8_t* v_exp, const int32_t* kv_lens, void* k, void* v, int B,
+                        int Hkv, int Lk, int d, const PagedKv& pg, void* stream) {
+  attn::CacheParams p;
+  const attn_status_t vs =
+      cache_params(k_codes, v_codes, k_exp, v_exp, kv_lens, B, Hkv, Lk, d, pg, &p);
+  if (vs != ATTN_OK) return vs;
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return ATTN_ERR_INVALID_ARG;
+  if ((long long)B * Hkv > 0x7fffffffLL / Lk) return ATTN_ERR_UNSUPPORTED;
+  p.k_out = k;
+  p.v_out = v;
+  p.err = error_word_for_current_device();
+  if (!p.err) return ATTN_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      d == 64 ? attn::launch_cache_read<64>(p, st) : attn::launch_cache_read<128>(p, st);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status_t decode_q8_impl(const void* q, const void* k_codes, const void* v_codes,
+                             const uint8_t* k_exp, const uint8_t* v_exp, void* o, float* lse,
+                             const int32_t* kv_lens, int B, int Hq, int Hkv, int Lq, int Lk_max,
+                             int d, float scale, int num_splits, void* workspace, size_t ws_bytes,
+                             void* stream, const PagedKv& pg) {
+  if (!q || !k_codes || !v_codes || !k_exp || !v_exp || !o || !lse || !kv_lens)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(o, 16) ||
+      !aligned(lse, 4) || !aligned(kv_lens, 4))
+    return ATTN_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  SplitPlan pl;
+  if (!plan_splits(B, Hq, Hkv, Lq, Lk_max, d, num_splits, &pl)) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)B * Hq > 0x7fffffffLL / Lq) return ATTN_ERR_UNSUPPORTED;
+  const long long nrows = (long long)B * Hq * Lq;
+  const size_t need = attn_decode_workspace_size(B, Hq, Hkv, Lq, Lk_max, d, num_splits);
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < need) return ATTN_ERR_WORKSPACE;
+
+  attn::DecodeQ8Params p;
+  std::memset(&p, 0, sizeof p);
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.ws_o = reinterpret_cast<float*>(workspace);
+  p.ws_lse = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) +
+                                      ws_lse_offset(pl, nrows, d));
+  p.k_exp = k_exp;
+  p.v_exp = v_exp;
+  p.kv_lens = kv_lens;
+  p.block_table = pg.block_table;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.Lq = Lq;
+  p.Lk = Lk_max;
+  p.group = Hq / Hkv;
+  p.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+  p.chunk = pl.chunk;
+  p.nsplit = pl.nsplit;
+  p.page_size = pg.page_size;
+  p.page_shift = pg.block_table ? log2_of(pg.page_size) : 0;
+  p.pages_per_seq = pg.pages_per_seq;
+  p.num_pages = pg.num_pages;
+  p.err = error_word_for_current_device();
+  if (!p.err) return ATTN_ERR_CUDA;
+
+  CUtensorMap tk, tv;
+  const uint64_t rows = pg.block_table ? (uint64_t)pg.page_size : (uint64_t)Lk_max;
+  const uint64_t planes =
+      pg.block_table ? (uint64_t)pg.num_pages * (uint64_t)Hkv : (uint64_t)B * (uint64_t)Hkv;
+  const uint64_t dims[3] = {(uint64_t)d, rows, planes};
+  const int box = attn::decode_q8_box_rows(pg.block_table ? pg.page_size : 1 << 16);
+  if (!encode_codes(&tk, k_codes, dims, box) || !encode_codes(&tv, v_codes, dims, box))
+    return ATTN_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = d == 64 ? attn::launch_decode_q8<64>(tk, tv, p, st)
+                          : attn::launch_decode_q8<128>(tk, tv, p, st);
+  if (e != cudaSuccess) return ATTN_ERR_CUDA;
+  if (pl.nsplit == 1) return ATTN_OK;  // the only split wrote O and the LSE
+
+  FwdParams c;
+  std::memset(&c, 0, sizeof c);
+  c.o = o;
+  c.lse = lse;
+  c.ws_o = p.ws_o;
+  c.ws_lse = p.ws_lse;
+  c.B = B;
+  c.Hq = Hq;
+  c.Lq = Lq;
+  c.nsplit = pl.nsplit;
+  e = d == 64 ? attn::launch_combine<64>(c, st) : attn::launch_combine<128>(c, st);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status_t attn_cache_append_q8(const void* k, const void* v, void* k_cache, void* v_cache,
+                                   uint8_t* k_exp, uint8_t* v_exp, const int32_t* kv_lens,
+                                   const int32_t* new_lens, int B, int Hkv, int Ln, int Lk_max,
+                                   int d, void* stream) {
+  return append_impl(k, v, k_cache, v_cache, k_exp, v_exp, kv_lens, new_lens, B, Hkv, Ln, Lk_max,
+                     d, PagedKv{}, stream);
+}
+
+attn_status_t attn_cache_append_paged_q8(const void* k, const void* v, void* k_pages,
+                                         void* v_pages, uint8_t* k_exp, uint8_t* v_exp,
+                                         const int32_t* block_table, const int32_t* kv_lens,
+                                         const int32_t* new_lens, int B, int Hkv, int Ln,
+                                         int page_size, int pages_per_seq, int num_pages, int d,
+                                         void* stream) {
+  PagedKv pg;
+  int lk = 0;
+  const attn_status_t st =
+      parse_paged(block_table, Hkv, page_size, pages_per_seq, num_pages, &pg, &lk);
+  if (st != ATTN_OK) return st;
+  return append_impl(k, v, k_pages, v_pages, k_exp, v_exp, kv_lens, new_lens, B, Hkv, Ln, lk, d,
+                     pg, stream);
+}
+
+attn_status_t attn_cache_read_q8(const void* k_cache, const void* v_cache, const uint8_t* k_exp,
+                                 const uint8_t* v_exp, const int32_t* kv_lens, void* k, void* v,
+                                 int B, int Hkv, int Lk_max, int d, void* stream) {
+  return read_impl(k_cache, v_cache, k_exp, v_exp, kv_lens, k, v, B, Hkv, Lk_max, d, PagedKv{},
+                   stream);
+}
+
+attn_status_t attn_cache_read_paged_q8(const void* k_pages, const void* v_pages,
+                                       const uint8_t* k_exp, const uint8_t* v_exp,
+                                       const int32_t* block_table, const int32_t* kv_lens,
+                                       void* k, void* v, int B, int Hkv, int page_size,
+                                       int pages_per_seq, int num_pages, int d, void* stream) {
+  PagedKv pg;
+  int lk = 0;
+  const attn_status_t st =
+      parse_paged(block_table, Hkv, page_size, pages_per_seq, num_pages, &pg, &lk);
+  if (st != ATTN_OK) return st;
+  return read_impl(k_pages, v_pages, k_exp, v_exp, kv_lens, k, v, B, Hkv, lk, d, pg, stream);
+}
+
+attn_status_t attn_decode_splitkv_q8(const void* q, const void* k_cache, const void* v_cache,
+                                     const uint8_t* k_exp, const uint8_t* v_exp, void* o,
+                                     float* lse, const int32_t* kv_lens, int B, int Hq, int Hkv,
+                                     int Lq, int Lk_max, int d, float scale, int num_splits,
+                                     void* workspace, size_t ws_bytes, void* stream) {
+  return decode_q8_impl(q, k_cache, v_cache, k_exp, v_exp, o, lse, kv_lens, B, Hq, Hkv, Lq,
+                        Lk_max, d, scale, num_splits, workspace, ws_bytes, stream, PagedKv{});
+}
+
+attn_status_t attn_decode_paged_q8(const void* q, const void* k_pages, const void* v_pages,
+                                   const uint8_t* k_exp, const uint8_t* v_exp,
+                                   const int32_t* block_table, void* o, float* lse,
+                                   const int32_t* kv_lens, int B, int Hq, int Hkv, int Lq,
+                                   int page_size, int pages_per_seq, int num_pages, int d,
+                                   float scale, int num_splits, void* workspace, size_t ws_bytes,
+                                   void* stream) {
+  PagedKv pg;
+  int lk = 0;
+  const attn_status_t st =
+      parse_paged(block_table, Hkv, page_size, pages_per_seq, num_pages, &pg, &lk);
+  if (st != ATTN_OK) return st;
+  return decode_q8_impl(q, k_pages, v_pages, k_exp, v_exp, o, lse, kv_lens, B, Hq, Hkv, Lq, lk, d,
+                        scale, num_splits, workspace, ws_bytes, stream, pg);
+}
+
+}  // extern "C"
+
+extern "C" {
 
 attn_status_t attn_get_device_error(void* stream, int* raw_bits) {
   if (raw_bits) *raw_bits = 0;
