@@ -378,6 +378,75 @@ attn_status_t attn_decode_paged_score_mod(const void* q, const void* k_pages, co
                                           void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * attn_decode_shared_prefix_num_splits — how many splits of the prefix
+ * attn_decode_shared_prefix uses: chunks of *chunk_keys keys (a whole number of
+ * 128-key tiles).  num_splits > 0 asks for that many (capped at ceil(Lp / 128)),
+ * 0 lets the library choose.  Returns -1 for invalid arguments.
+ *
+ * attn_decode_shared_prefix_workspace_size — bytes of caller workspace it needs:
+ * the partials of the prefix's splits, then those of the sequences' own caches
+ * (split as attn_decode_splitkv does with num_splits = 0), laid out as
+ * attn_decode_workspace_size describes.  0 for invalid arguments.
+ */
+int attn_decode_shared_prefix_num_splits(int B, int Hq, int Hkv, int Lq, int Lp, int num_splits,
+                                         int* chunk_keys);
+size_t attn_decode_shared_prefix_workspace_size(int B, int Hq, int Hkv, int Lq, int Lp, int Lk_max,
+                                                int d, int num_splits);
+
+/*
+ * attn_decode_shared_prefix — split-KV decode of a batch whose sequences share
+ * one prefix (a system prompt, a document) and go on with a cache of their own.
+ * (No counterpart on the pages: the split and merge of attn_decode_splitkv with
+ * the prefix as splits that all sequences read together.)
+ *
+ * Defines: every query row of sequence b sees the Lp keys of the prefix and the
+ * first kv_lens[b] keys of its own cache; O and LSE are those of
+ * attn_decode_splitkv on the concatenation.  The prefix is read once for the
+ * whole batch, its query rows stacked into 128-row tiles across sequences; three
+ * launches on `stream`: the prefix's partials, the caches' partials, the combine.
+ *
+ * Arguments
+ *   q        [B, Hq, Lq, d] bf16, read;  o [B, Hq, Lq, d] bf16, lse [B, Hq, Lq]
+ *            fp32, written
+ *   k_prefix, v_prefix  [Hkv, Lp, d] bf16, read;  Lp >= 1
+ *   k_cache, v_cache    [B, Hkv, Lk_max, d] bf16, read only below kv_lens[b]
+ *   kv_lens  [B] int32 DEVICE array, each in [0, Lk_max] (0: the prefix alone); an
+ *            entry outside is clamped and flags the device error word
+ *   num_splits  of the prefix, as above;  d in {64, 128};  scale > 0
+ *   workspace, ws_bytes  caller-owned device buffer, 256-byte aligned, at least
+ *            attn_decode_shared_prefix_workspace_size(...) bytes, not shared with a
+ *            concurrent call
+ * Errors: INVALID_ARG / UNSUPPORTED / WORKSPACE before any launch; CUDA on
+ * launch failure.
+ */
+attn_status_t attn_decode_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix,
+                                        const void* k_cache, const void* v_cache, void* o,
+                                        float* lse, const int32_t* kv_lens, int B, int Hq, int Hkv,
+                                        int Lq, int Lp, int Lk_max, int d, float scale,
+                                        int num_splits, void* workspace, size_t ws_bytes,
+                                        void* stream);
+
+/*
+ * attn_decode_shared_prefix_paged — attn_decode_shared_prefix with the prefix and
+ * the caches in one page pool.
+ *
+ *   k_pages, v_pages  [num_pages, Hkv, page_size, d] bf16, read
+ *   prefix_table  [ceil(Lp / page_size)] int32 DEVICE array: the prefix's pages in
+ *            order; rows of the last page past Lp may hold anything
+ *   block_table   [B, pages_per_seq] int32 DEVICE array: the pages of the
+ *            sequences' own caches (key 0 is the first key after the prefix)
+ *   page_size, pages_per_seq, num_pages  as attn_decode_paged; Lk_max =
+ *            pages_per_seq * page_size
+ * An out-of-range page id of the prefix reads as zeros and flags the device error
+ * word (ATTN_ERR_INVALID_ARG).  The other arguments and errors as above.
+ */
+attn_status_t attn_decode_shared_prefix_paged(
+    const void* q, const void* k_pages, const void* v_pages, const int32_t* prefix_table,
+    const int32_t* block_table, void* o, float* lse, const int32_t* kv_lens, int B, int Hq,
+    int Hkv, int Lq, int Lp, int page_size, int pages_per_seq, int num_pages, int d, float scale,
+    int num_splits, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * The 8-bit KV cache (attn_cache_*_q8, attn_decode_*_q8).  (No counterpart on
  * the pages: the serving-side form of the cache the decode reads.)
  *

@@ -9,6 +9,7 @@ Entry points (same names as the C ABI):
   attn_fwd(q, k, v, ...)                 -> (o, lse)
   attn_fwd_host(q, k, v, ...)            -> (o, lse)   host tensors in and out
   attn_decode_splitkv(q, k, v, kv_lens, ...) -> (o, lse)
+  attn_decode_shared_prefix(q, k_prefix, v_prefix, k_cache, v_cache, kv_lens, ...) -> (o, lse)
   attn_cache_append_q8(k, v, k_cache, v_cache, k_exp, v_exp, kv_lens, ...)   8-bit cache, in place
   attn_cache_read_q8(k_cache, v_cache, k_exp, v_exp, kv_lens, ...) -> (k, v)
   attn_decode_splitkv_q8(q, k_cache, v_cache, k_exp, v_exp, kv_lens, ...) -> (o, lse)
@@ -35,6 +36,8 @@ __all__ = [
     "attn_decode_num_splits", "SCORE_MOD_NONE", "SCORE_MOD_ALIBI", "SCORE_MOD_REL_BIAS",
     "attn_decode_workspace_size", "attn_decode_paged", "attn_decode_splitkv_noalloc",
     "attn_decode_splitkv_score_mod", "attn_decode_paged_score_mod",
+    "attn_decode_shared_prefix", "attn_decode_shared_prefix_paged",
+    "attn_decode_shared_prefix_num_splits", "attn_decode_shared_prefix_workspace_size",
     "attn_cache_append_q8", "attn_cache_append_paged_q8", "attn_cache_read_q8",
     "attn_cache_read_paged_q8", "attn_decode_splitkv_q8", "attn_decode_paged_q8",
     "attn_get_device_error", "attn_selftest_wait_timeout", "attn_status_string",
@@ -63,6 +66,8 @@ EXPORTED_SYMBOLS = (
     "attn_decode_num_splits", "attn_decode_workspace_size",
     "attn_decode_splitkv", "attn_decode_paged", "attn_decode_splitkv_noalloc",
     "attn_decode_splitkv_score_mod", "attn_decode_paged_score_mod",
+    "attn_decode_shared_prefix", "attn_decode_shared_prefix_paged",
+    "attn_decode_shared_prefix_num_splits", "attn_decode_shared_prefix_workspace_size",
     "attn_cache_append_q8", "attn_cache_append_paged_q8", "attn_cache_read_q8",
     "attn_cache_read_paged_q8", "attn_decode_splitkv_q8", "attn_decode_paged_q8",
     "attn_get_device_error", "attn_selftest_wait_timeout", "attn_status_string",
@@ -138,6 +143,15 @@ def load_library():
         lib.attn_decode_splitkv_noalloc.argtypes = [P, P, P, P, P, P, i32, i32, i32, i32, i32,
                                                     i32, f32, i32, P]
         lib.attn_decode_splitkv_noalloc.restype = i32
+        lib.attn_decode_shared_prefix_num_splits.argtypes = \
+            [i32] * 6 + [ctypes.POINTER(ctypes.c_int)]
+        lib.attn_decode_shared_prefix_num_splits.restype = i32
+        lib.attn_decode_shared_prefix_workspace_size.argtypes = [i32] * 8
+        lib.attn_decode_shared_prefix_workspace_size.restype = sz
+        lib.attn_decode_shared_prefix.argtypes = [P] * 8 + [i32] * 7 + [f32, i32, P, sz, P]
+        lib.attn_decode_shared_prefix.restype = i32
+        lib.attn_decode_shared_prefix_paged.argtypes = [P] * 8 + [i32] * 9 + [f32, i32, P, sz, P]
+        lib.attn_decode_shared_prefix_paged.restype = i32
         lib.attn_cache_append_q8.argtypes = [P] * 8 + [i32] * 5 + [P]
         lib.attn_cache_append_q8.restype = i32
         lib.attn_cache_append_paged_q8.argtypes = [P] * 9 + [i32] * 7 + [P]
@@ -603,6 +617,104 @@ def _check_q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, B):
     if block_table is not None:
         _check("block_table", block_table, torch.int32, block_table.shape, dev)
     _check("kv_lens", kv_lens, torch.int32, (B,), dev)
+
+
+def attn_decode_shared_prefix_num_splits(B, Hq, Hkv, Lq, Lp, num_splits=0):
+    """(splits, chunk_keys) of the prefix that attn_decode_shared_prefix uses."""
+    chunk = ctypes.c_int(0)
+    n = load_library().attn_decode_shared_prefix_num_splits(B, Hq, Hkv, Lq, Lp, num_splits,
+                                                            ctypes.byref(chunk))
+    if n < 0:
+        raise AttnError(ATTN_ERR_INVALID_ARG, "attn_decode_shared_prefix_num_splits")
+    return int(n), int(chunk.value)
+
+
+def attn_decode_shared_prefix_workspace_size(B, Hq, Hkv, Lq, Lp, Lk_max, d, num_splits=0) -> int:
+    n = load_library().attn_decode_shared_prefix_workspace_size(B, Hq, Hkv, Lq, Lp, Lk_max, d,
+                                                                num_splits)
+    if n == 0:
+        raise AttnError(ATTN_ERR_INVALID_ARG, "attn_decode_shared_prefix_workspace_size")
+    return int(n)
+
+
+def attn_decode_shared_prefix(q, k_prefix, v_prefix, k_cache, v_cache, kv_lens, *, scale=None,
+                              num_splits=0, workspace=None, o=None, lse=None, stream=None):
+    """Split-KV decode of a batch behind one shared prefix (see
+    ``attn_decode_shared_prefix`` in include/attn.h).
+
+    q: [B, Hq, Lq, d]; k_prefix/v_prefix: [Hkv, Lp, d], read by every sequence;
+    k_cache/v_cache: [B, Hkv, Lk_max, d], the sequences' own keys; kv_lens: [B] int32,
+    how many of those each has (0 allowed).  Returns (o, lse).
+    """
+    if not isinstance(k_prefix, torch.Tensor) or k_prefix.dim() != 3:
+        raise ValueError("k_prefix must be a [Hkv, Lp, d] CUDA tensor")
+    B, Hkv, Lk, d, _, _, _ = _cache_shape(k_cache, None)
+    for name, t in (("k_prefix", k_prefix), ("v_prefix", v_prefix)):
+        _check(name, t, torch.bfloat16, (Hkv, k_prefix.shape[1], d), k_cache.device)
+    return _shared_prefix(q, k_prefix, v_prefix, None, k_prefix.shape[1], k_cache, v_cache, None,
+                          kv_lens, scale, num_splits, workspace, o, lse, stream)
+
+
+def attn_decode_shared_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len, block_table,
+                                    kv_lens, *, scale=None, num_splits=0, workspace=None, o=None,
+                                    lse=None, stream=None):
+    """attn_decode_shared_prefix with prefix and caches in one page pool (see
+    ``attn_decode_shared_prefix_paged`` in include/attn.h).
+
+    k_pages/v_pages: [num_pages, Hkv, page_size, d]; prefix_table: int32, the
+    ceil(prefix_len / page_size) pages of the prefix; block_table: [B, pages_per_seq]
+    int32, the pages of the sequences' own keys.  Returns (o, lse).
+    """
+    if block_table is None:
+        raise ValueError("block_table must be an int32 CUDA tensor [B, pages_per_seq]")
+    page = _cache_shape(k_pages, block_table)[4]
+    _check("prefix_table", prefix_table, torch.int32, (-(-int(prefix_len) // max(page, 1)),),
+           k_pages.device)
+    return _shared_prefix(q, None, None, prefix_table, int(prefix_len), k_pages, v_pages,
+                          block_table, kv_lens, scale, num_splits, workspace, o, lse, stream)
+
+
+def _shared_prefix(q, k_prefix, v_prefix, prefix_table, Lp, k_cache, v_cache, block_table, kv_lens,
+                   scale, num_splits, workspace, o, lse, stream):
+    B, Hkv, Lk, d, page, per_seq, n_pages = _cache_shape(k_cache, block_table)
+    dev = k_cache.device
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check(name, t, torch.bfloat16, k_cache.shape, dev)
+    if block_table is not None:
+        _check("block_table", block_table, torch.int32, block_table.shape, dev)
+    _check("kv_lens", kv_lens, torch.int32, (B,), dev)
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a [B, Hq, Lq, d] CUDA tensor")
+    _, Hq, Lq, _ = q.shape
+    _check("q", q, torch.bfloat16, (B, Hq, Lq, d), dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    o = torch.empty_like(q) if o is None else o
+    _check("o", o, torch.bfloat16, q.shape, dev)
+    if lse is None:
+        lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=dev)
+    _check("lse", lse, torch.float32, (B, Hq, Lq), dev)
+    lib = load_library()
+    with _on(dev):
+        if workspace is None:
+            need = attn_decode_shared_prefix_workspace_size(B, Hq, Hkv, Lq, Lp, Lk, d, num_splits)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        tail = (float(scale), int(num_splits), _ptr(workspace),
+                workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
+        if block_table is None:
+            name = "attn_decode_shared_prefix"
+            st = lib.attn_decode_shared_prefix(
+                _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k_cache), _ptr(v_cache), _ptr(o),
+                _ptr(lse), _ptr(kv_lens), B, Hq, Hkv, Lq, Lp, Lk, d, *tail)
+        else:
+            name = "attn_decode_shared_prefix_paged"
+            st = lib.attn_decode_shared_prefix_paged(
+                _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_table), _ptr(block_table),
+                _ptr(o), _ptr(lse), _ptr(kv_lens), B, Hq, Hkv, Lq, Lp, page, per_seq, n_pages, d,
+                *tail)
+    if st != ATTN_OK:
+        raise AttnError(st, name)
+    return o, lse
 
 
 def attn_cache_append_q8(k, v, k_cache, v_cache, k_exp, v_exp, kv_lens, *, new_lens=None,

@@ -14,6 +14,7 @@
 #include "attn.h"
 #include "attn_bwd_params.h"
 #include "attn_params.h"
+#include "attn_prefix_params.h"
 #include "cache_q8_params.h"
 #include "host_once.h"
 
@@ -44,6 +45,9 @@ template <int D>
 cudaError_t launch_decode_q8(const CUtensorMap&, const CUtensorMap&, const DecodeQ8Params&,
                              cudaStream_t);
 int decode_q8_box_rows(int page_size);
+template <int D>
+cudaError_t launch_prefix(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                          const PrefixParams&, cudaStream_t);
 }  // namespace attn
 
 namespace {
@@ -105,9 +109,11 @@ struct TmapKey {
   const void* base;
   uint64_t dims[3];
   int rank, box_rows, kind;
+  uint64_t dim3 = 0;  // fourth dimension
   bool operator==(const TmapKey& o) const {
     return base == o.base && rank == o.rank && box_rows == o.box_rows && kind == o.kind &&
-           dims[0] == o.dims[0] && dims[1] == o.dims[1] && dims[2] == o.dims[2];
+           dims[0] == o.dims[0] && dims[1] == o.dims[1] && dims[2] == o.dims[2] &&
+           dim3 == o.dim3;
   }
 };
 constexpr int kTmapCacheSize = 16;
@@ -194,6 +200,29 @@ bool encode_bf16_packed(CUtensorMap* map, const void* base, int d, int H, int to
     cuuint32_t box[3] = {64, 1, (cuuint32_t)kBlockN};
     cuuint32_t estride[3] = {1, 1, 1};
     CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3u, const_cast<void*>(base), gdim,
+                    gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+  });
+}
+
+// Query rows of a KV head across sequences: q [B, Hkv, G, d] as {d, G, Hkv, B},
+// boxes of 64 columns by box_g rows of one head of box_b sequences (rows of
+// consecutive sequences land one after another).
+bool encode_bf16_rows(CUtensorMap* map, const void* base, int d, int G, int Hkv, int B, int box_g,
+                      int box_b) {
+  TmapKey key{base, {(uint64_t)d, (uint64_t)G, (uint64_t)Hkv}, 4, box_g * 256 + box_b, 4,
+              (uint64_t)B};
+  return cached_encode(map, key, [&](CUtensorMap* out) {
+    auto fn = get_encode_fn();
+    if (!fn) return false;
+    cuuint64_t gdim[4] = {(cuuint64_t)d, (cuuint64_t)G, (cuuint64_t)Hkv, (cuuint64_t)B};
+    cuuint64_t row = (cuuint64_t)d * 2;
+    cuuint64_t gstride[3] = {row, row * G, row * G * Hkv};
+    cuuint32_t box[4] = {64, (cuuint32_t)box_g, 1, (cuuint32_t)box_b};
+    cuuint32_t estride[4] = {1, 1, 1, 1};
+    CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4u, const_cast<void*>(base), gdim,
                     gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -849,6 +878,60 @@ struct PagedKv {
   int num_pages = 0;
 };
 
+// Fills the launch parameters of the split-KV decode except outputs, workspace
+// and score modifier.
+void set_decode_shape(FwdParams* p, const int32_t* kv_lens, int B, int Hq, int Hkv, int Lq,
+                      int Lk_max, float scale, const SplitPlan& pl, const PagedKv& pg) {
+  p->kv_lens = kv_lens;
+  p->B = B;
+  p->Hq = Hq;
+  p->Hkv = Hkv;
+  p->Lq = Lq;
+  p->Lk = Lk_max;
+  p->group = Hq / Hkv;
+  p->mask_kind = ATTN_MASK_NONE;
+  p->window_l = -1;
+  p->window_r = -1;
+  p->draft_block = 1;
+  p->scale_log2 = (float)((double)scale * 1.4426950408889634074);
+  p->chunk = pl.chunk;
+  p->nsplit = pl.nsplit;
+  p->row_tiles = pl.row_tiles;
+  p->block_table = pg.block_table;
+  p->page_size = pg.page_size;
+  p->pages_per_seq = pg.pages_per_seq;
+  p->num_pages = pg.num_pages;
+}
+
+// Tensor maps of a bf16 K/V cache: contiguous [planes, rows, d] or a page pool,
+// boxes of at most 128 rows.
+bool encode_kv(CUtensorMap* tk, CUtensorMap* tv, const void* k, const void* v, int d,
+               uint64_t rows, uint64_t planes, const PagedKv& pg, int Hkv) {
+  if (pg.block_table) {
+    const uint64_t dk[3] = {(uint64_t)d, (uint64_t)pg.page_size,
+                            (uint64_t)pg.num_pages * (uint64_t)Hkv};
+    const int box = pg.page_size < kBlockN ? pg.page_size : kBlockN;
+    return encode_bf16(tk, k, 3, dk, box) && encode_bf16(tv, v, 3, dk, box);
+  }
+  const uint64_t dk[3] = {(uint64_t)d, rows, planes};
+  return encode_bf16(tk, k, 3, dk) && encode_bf16(tv, v, 3, dk);
+}
+
+// The partial kernel of the split-KV decode for launch parameters p.
+attn_status_t launch_split_decode(const FwdParams& p, const void* q, const void* k_cache,
+                                  const void* v_cache, int d, const PagedKv& pg,
+                                  cudaStream_t st) {
+  CUtensorMap tq, tk, tv;
+  const uint64_t dq[2] = {(uint64_t)d, (uint64_t)p.B * p.Hq * p.Lq};
+  if (!encode_bf16(&tq, q, 2, dq)) return ATTN_ERR_CUDA;
+  if (!encode_kv(&tk, &tv, k_cache, v_cache, d, (uint64_t)p.Lk, (uint64_t)p.B * p.Hkv, pg, p.Hkv))
+    return ATTN_ERR_CUDA;
+  dim3 grid((unsigned)p.nsplit, (unsigned)(p.B * p.Hkv * p.row_tiles), 1);
+  const cudaError_t e = d == 64 ? attn::launch_decode<64>(tq, tk, tv, p, grid, st)
+                                : attn::launch_decode<128>(tq, tk, tv, p, grid, st);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 // Shared body of the contiguous and paged split-KV decode.
 attn_status_t decode_impl(const void* q, const void* k_cache, const void* v_cache, void* o,
                           float* lse, const int32_t* kv_lens, int B, int Hq, int Hkv, int Lq,
@@ -876,50 +959,15 @@ attn_status_t decode_impl(const void* q, const void* k_cache, const void* v_cach
   p.ws_o = reinterpret_cast<float*>(workspace);
   p.ws_lse = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) +
                                       ws_lse_offset(pl, nrows, d));
-  p.kv_lens = kv_lens;
-  p.B = B;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.Lq = Lq;
-  p.Lk = Lk_max;
-  p.group = Hq / Hkv;
-  p.mask_kind = ATTN_MASK_NONE;
-  p.window_l = -1;
-  p.window_r = -1;
-  p.draft_block = 1;
-  p.scale_log2 = (float)((double)scale * 1.4426950408889634074);
-  p.chunk = pl.chunk;
-  p.nsplit = pl.nsplit;
-  p.row_tiles = pl.row_tiles;
+  set_decode_shape(&p, kv_lens, B, Hq, Hkv, Lq, Lk_max, scale, pl, pg);
   p.alibi_slopes = sm.alibi_slopes;
   p.rel_table = sm.rel_table;
   p.rel_max = sm.rel_max;
-  p.block_table = pg.block_table;
-  p.page_size = pg.page_size;
-  p.pages_per_seq = pg.pages_per_seq;
-  p.num_pages = pg.num_pages;
 
-  CUtensorMap tq, tk, tv;
-  const uint64_t dq[2] = {(uint64_t)d, (uint64_t)nrows};
-  if (!encode_bf16(&tq, q, 2, dq)) return ATTN_ERR_CUDA;
-  if (pg.block_table) {
-    const uint64_t dk[3] = {(uint64_t)d, (uint64_t)pg.page_size,
-                            (uint64_t)pg.num_pages * (uint64_t)Hkv};
-    const int rows = pg.page_size < kBlockN ? pg.page_size : kBlockN;
-    if (!encode_bf16(&tk, k_cache, 3, dk, rows) || !encode_bf16(&tv, v_cache, 3, dk, rows))
-      return ATTN_ERR_CUDA;
-  } else {
-    const uint64_t dk[3] = {(uint64_t)d, (uint64_t)Lk_max, (uint64_t)B * Hkv};
-    if (!encode_bf16(&tk, k_cache, 3, dk) || !encode_bf16(&tv, v_cache, 3, dk))
-      return ATTN_ERR_CUDA;
-  }
-
-  dim3 grid((unsigned)pl.nsplit, (unsigned)(B * Hkv * pl.row_tiles), 1);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = d == 64 ? attn::launch_decode<64>(tq, tk, tv, p, grid, st)
-                          : attn::launch_decode<128>(tq, tk, tv, p, grid, st);
-  if (e != cudaSuccess) return ATTN_ERR_CUDA;
-  e = d == 64 ? attn::launch_combine<64>(p, st) : attn::launch_combine<128>(p, st);
+  const attn_status_t ds = launch_split_decode(p, q, k_cache, v_cache, d, pg, st);
+  if (ds != ATTN_OK) return ds;
+  const cudaError_t e = d == 64 ? attn::launch_combine<64>(p, st) : attn::launch_combine<128>(p, st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -1013,6 +1061,200 @@ attn_status_t attn_decode_paged_score_mod(const void* q, const void* k_pages, co
   return paged_impl(q, k_pages, v_pages, block_table, o, lse, kv_lens, B, Hq, Hkv, Lq, page_size,
                     pages_per_seq, num_pages, d, scale, num_splits, workspace, ws_bytes, stream,
                     sm);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------- shared prefix
+namespace {
+
+// Splits of the prefix: row tiles (128 rows of one KV head, whatever their
+// sequence) in pairs, and np chunks of whole key tiles.
+struct PrefixPlan {
+  int nb, per_seq, tiles, pairs, box_rows;
+  int np, chunk;
+};
+
+bool plan_prefix(int B, int Hq, int Hkv, int Lq, int Lp, int num_splits, PrefixPlan* pp) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Lq < 1 || Lp < 1 || num_splits < 0 || Hq % Hkv) return false;
+  const long long G = (long long)(Hq / Hkv) * Lq;
+  if (G > 0x7fffffffLL / 2) return false;
+  pp->nb = G <= kBlockM ? (int)std::min<long long>(kBlockM / G, B) : 1;
+  pp->per_seq = (int)ceil_div(G, kBlockM);
+  const long long tiles = G <= kBlockM ? ceil_div(B, pp->nb) : (long long)B * pp->per_seq;
+  if (tiles > 0x7fffffffLL) return false;
+  pp->tiles = (int)tiles;
+  pp->pairs = (int)ceil_div(tiles, 2);
+  pp->box_rows = G <= kBlockM ? (int)G * pp->nb : kBlockM;
+  const long long key_tiles = ceil_div(Lp, kBlockN);
+  const long long units = (long long)Hkv * pp->pairs;
+  long long np = std::min<long long>(num_splits, key_tiles);
+  if (num_splits == 0) {
+    // The count with the least time in units of one key tile of a CTA: rounds of
+    // CTAs over the SMs times (tiles per CTA + about 4 for its start and end),
+    // plus each split's partial rows, written here and read by the combine
+    // (1 KB per row and split at d = 128, about 1 us per key tile and CTA).
+    const double sms = num_sms(), rows = (double)B * Hq * Lq;
+    double best = 0;
+    const long long most = std::min<long long>(key_tiles, ceil_div(4 * num_sms(), units));
+    for (long long n = 1; n <= most; ++n) {
+      const double cost = (double)ceil_div(units * n, (long long)sms) *
+                              ((double)ceil_div(key_tiles, n) + 4.0) +
+                          (double)n * rows * 1.5e-4;
+      if (n == 1 || cost < best) {
+        best = cost;
+        np = n;
+      }
+    }
+  }
+  pp->chunk = (int)(ceil_div(key_tiles, np) * kBlockN);
+  pp->np = (int)ceil_div(Lp, pp->chunk);
+  return true;
+}
+
+struct PrefixCall {
+  PrefixPlan pp;
+  SplitPlan pl;  // of the sequences' own caches
+  long long nrows;
+  size_t bytes;
+};
+
+bool plan_prefix_call(int B, int Hq, int Hkv, int Lq, int Lp, int Lk_max, int d, int num_splits,
+                      PrefixCall* pc) {
+  if (!plan_prefix(B, Hq, Hkv, Lq, Lp, num_splits, &pc->pp)) return false;
+  if (!plan_splits(B, Hq, Hkv, Lq, Lk_max, d, 0, &pc->pl)) return false;
+  if ((long long)B * Hq > 0x7fffffffLL / Lq) return false;
+  pc->nrows = (long long)B * Hq * Lq;
+  SplitPlan all = pc->pl;
+  all.nsplit += pc->pp.np;
+  pc->bytes = ws_lse_offset(all, pc->nrows, d) + (size_t)all.nsplit * (size_t)pc->nrows * 4;
+  return true;
+}
+
+attn_status_t shared_prefix_impl(const void* q, const void* k_prefix, const void* v_prefix,
+                                 const int32_t* prefix_table, const void* k_cache,
+                                 const void* v_cache, void* o, float* lse, const int32_t* kv_lens,
+                                 int B, int Hq, int Hkv, int Lq, int Lp, int Lk_max, int d,
+                                 float scale, int num_splits, void* workspace, size_t ws_bytes,
+                                 void* stream, const PagedKv& pg) {
+  if (!q || !k_prefix || !v_prefix || !k_cache || !v_cache || !o || !lse || !kv_lens)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_prefix, 16) || !aligned(v_prefix, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
+      !aligned(kv_lens, 4))
+    return ATTN_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if (B < 1 || Hq < 1 || Hkv < 1 || Lq < 1 || Lp < 1 || Lk_max < 1 || num_splits < 0 || Hq % Hkv)
+    return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  PrefixCall pc;
+  if (!plan_prefix_call(B, Hq, Hkv, Lq, Lp, Lk_max, d, num_splits, &pc))
+    return ATTN_ERR_UNSUPPORTED;
+  if (pc.pl.chunk / kBlockN > attn::kMaxKvTiles) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)B * Hkv * pc.pl.row_tiles > kMaxGridY) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)Hkv * pc.pp.pairs * pc.pp.np > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < pc.bytes) return ATTN_ERR_WORKSPACE;
+  int* err = error_word_for_current_device();
+  if (!err) return ATTN_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int np = pc.pp.np, G = Hq / Hkv * Lq;
+  SplitPlan all = pc.pl;
+  all.nsplit += np;
+
+  // partials: splits [0, np) the prefix, [np, np + nsplit) the sequences' own caches
+  FwdParams p;
+  std::memset(&p, 0, sizeof p);
+  set_decode_shape(&p, kv_lens, B, Hq, Hkv, Lq, Lk_max, scale, pc.pl, pg);
+  float* ws_o = reinterpret_cast<float*>(workspace);
+  float* ws_lse = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) +
+                                           ws_lse_offset(all, pc.nrows, d));
+  attn::PrefixParams x;
+  std::memset(&x, 0, sizeof x);
+  x.ws_o = ws_o;
+  x.ws_lse = ws_lse;
+  x.err = err;
+  x.prefix_table = prefix_table;
+  x.nrows = pc.nrows;
+  x.B = B;
+  x.Hkv = Hkv;
+  x.G = G;
+  x.Lp = Lp;
+  x.nb = pc.pp.nb;
+  x.per_seq = pc.pp.per_seq;
+  x.tiles = pc.pp.tiles;
+  x.pairs = pc.pp.pairs;
+  x.box_rows = pc.pp.box_rows;
+  x.chunk = pc.pp.chunk;
+  x.nsplit = np;
+  x.page_size = pg.page_size;
+  x.num_pages = pg.num_pages;
+  x.scale_log2 = p.scale_log2;
+  CUtensorMap tq, tk, tv;
+  if (!encode_bf16_rows(&tq, q, d, G, Hkv, B, std::min(G, kBlockM), pc.pp.nb)) return ATTN_ERR_CUDA;
+  if (!encode_kv(&tk, &tv, k_prefix, v_prefix, d, (uint64_t)Lp, (uint64_t)Hkv, pg, Hkv))
+    return ATTN_ERR_CUDA;
+  cudaError_t e = d == 64 ? attn::launch_prefix<64>(tq, tk, tv, x, st)
+                          : attn::launch_prefix<128>(tq, tk, tv, x, st);
+  if (e != cudaSuccess) return ATTN_ERR_CUDA;
+
+  p.ws_o = ws_o + (size_t)np * (size_t)pc.nrows * d;
+  p.ws_lse = ws_lse + (size_t)np * (size_t)pc.nrows;
+  const attn_status_t ds = launch_split_decode(p, q, k_cache, v_cache, d, pg, st);
+  if (ds != ATTN_OK) return ds;
+
+  p.o = o;
+  p.lse = lse;
+  p.ws_o = ws_o;
+  p.ws_lse = ws_lse;
+  p.nsplit = all.nsplit;
+  e = d == 64 ? attn::launch_combine<64>(p, st) : attn::launch_combine<128>(p, st);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_decode_shared_prefix_num_splits(int B, int Hq, int Hkv, int Lq, int Lp, int num_splits,
+                                         int* chunk_keys) {
+  PrefixPlan pp;
+  if (!plan_prefix(B, Hq, Hkv, Lq, Lp, num_splits, &pp)) return -1;
+  if (chunk_keys) *chunk_keys = pp.chunk;
+  return pp.np;
+}
+
+size_t attn_decode_shared_prefix_workspace_size(int B, int Hq, int Hkv, int Lq, int Lp, int Lk_max,
+                                                int d, int num_splits) {
+  PrefixCall pc;
+  if (!plan_prefix_call(B, Hq, Hkv, Lq, Lp, Lk_max, d, num_splits, &pc)) return 0;
+  return pc.bytes;
+}
+
+attn_status_t attn_decode_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix,
+                                        const void* k_cache, const void* v_cache, void* o,
+                                        float* lse, const int32_t* kv_lens, int B, int Hq, int Hkv,
+                                        int Lq, int Lp, int Lk_max, int d, float scale,
+                                        int num_splits, void* workspace, size_t ws_bytes,
+                                        void* stream) {
+  return shared_prefix_impl(q, k_prefix, v_prefix, nullptr, k_cache, v_cache, o, lse, kv_lens, B,
+                            Hq, Hkv, Lq, Lp, Lk_max, d, scale, num_splits, workspace, ws_bytes,
+                            stream, PagedKv{});
+}
+
+attn_status_t attn_decode_shared_prefix_paged(
+    const void* q, const void* k_pages, const void* v_pages, const int32_t* prefix_table,
+    const int32_t* block_table, void* o, float* lse, const int32_t* kv_lens, int B, int Hq,
+    int Hkv, int Lq, int Lp, int page_size, int pages_per_seq, int num_pages, int d, float scale,
+    int num_splits, void* workspace, size_t ws_bytes, void* stream) {
+  PagedKv pg;
+  int lk = 0;
+  if (!prefix_table || !aligned(prefix_table, 4)) return ATTN_ERR_INVALID_ARG;
+  const attn_status_t st =
+      parse_paged(block_table, Hkv, page_size, pages_per_seq, num_pages, &pg, &lk);
+  if (st != ATTN_OK) return st;
+  return shared_prefix_impl(q, k_pages, v_pages, prefix_table, k_pages, v_pages, o, lse, kv_lens,
+                            B, Hq, Hkv, Lq, Lp, lk, d, scale, num_splits, workspace, ws_bytes,
+                            stream, pg);
 }
 
 }  // extern "C"

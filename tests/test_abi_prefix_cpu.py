@@ -1,0 +1,93 @@
+"""The shared-prefix decode's entry points without a GPU: the plan, the workspace's
+arithmetic and host-side rejection."""
+import ctypes
+
+import pytest
+
+import sm_attn_fwd_b200 as ab
+
+A = ctypes.c_void_p(0x10000)
+M = ctypes.c_void_p(0x10008)
+INV, UNS, WSP = ab.ATTN_ERR_INVALID_ARG, ab.ATTN_ERR_UNSUPPORTED, ab.ATTN_ERR_WORKSPACE
+
+
+def call(paged=False, **kw):
+    a = dict(q=A, kp=A, vp=A, pt=A, k=A, v=A, bt=A, o=A, lse=A, kv=A, B=4, Hq=16, Hkv=2, Lq=1,
+             Lp=1000, Lk=64, page=16, per=4, n=64, d=128, scale=0.1, ns=0,
+             ws=ctypes.c_void_p(0x100000), wsb=1 << 30)
+    a.update(kw)
+    lib = ab.load_library()
+    tail = (a["d"], a["scale"], a["ns"], a["ws"], a["wsb"], None)
+    if paged:
+        return lib.attn_decode_shared_prefix_paged(
+            a["q"], a["k"], a["v"], a["pt"], a["bt"], a["o"], a["lse"], a["kv"], a["B"], a["Hq"],
+            a["Hkv"], a["Lq"], a["Lp"], a["page"], a["per"], a["n"], *tail)
+    return lib.attn_decode_shared_prefix(a["q"], a["kp"], a["vp"], a["k"], a["v"], a["o"], a["lse"],
+                                         a["kv"], a["B"], a["Hq"], a["Hkv"], a["Lq"], a["Lp"],
+                                         a["Lk"], *tail)
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), INV), (dict(k=None), INV), (dict(v=M), INV), (dict(o=None), INV),
+    (dict(lse=ctypes.c_void_p(0x10002)), INV), (dict(kv=None), INV), (dict(B=0), INV),
+    (dict(Hq=15), INV), (dict(Lq=0), INV), (dict(Lp=0), INV), (dict(ns=-1), INV),
+    (dict(scale=0.0), INV), (dict(scale=float("nan")), INV), (dict(d=96), UNS), (dict(ws=None), WSP),
+    (dict(ws=ctypes.c_void_p(0x100010)), WSP), (dict(wsb=1000), WSP)])
+def test_rejects_on_host(paged, kw, status):
+    assert call(paged, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(pt=None), INV), (dict(pt=ctypes.c_void_p(0x10002)), INV), (dict(bt=None), INV),
+    (dict(page=24), INV), (dict(per=0), INV), (dict(n=0), INV), (dict(page=65536, per=32768), UNS)])
+def test_paged_rejects_on_host(kw, status):
+    assert call(True, **kw) == status
+
+
+def test_contiguous_rejects_on_host():
+    assert call(kp=None) == INV and call(vp=M) == INV and call(Lk=0) == INV
+
+
+def plan(*args):
+    chunk = ctypes.c_int(0)
+    n = ab.load_library().attn_decode_shared_prefix_num_splits(*args, ctypes.byref(chunk))
+    return n, chunk.value
+
+
+def test_split_plan_covers_the_prefix():
+    for B, Hq, Hkv, Lq in ((1, 1, 1, 1), (4, 32, 8, 1), (64, 64, 8, 1), (64, 64, 8, 16),
+                           (3, 6, 2, 50)):
+        for Lp in (1, 127, 128, 129, 2064, 32768, 100001):
+            for ns in (0, 1, 3, 1 << 20):
+                n, chunk = plan(B, Hq, Hkv, Lq, Lp, ns)
+                assert chunk % 128 == 0 and n * chunk >= Lp and (n - 1) * chunk < Lp
+                if ns:
+                    assert n <= ns
+    assert plan(4, 16, 2, 1, 1000, 3) == (3, 384)
+    assert plan(4, 16, 2, 1, 1000, 100) == (8, 128)
+    assert plan(0, 16, 2, 1, 1000, 0)[0] == -1 and plan(4, 15, 2, 1, 1000, 0)[0] == -1
+    assert plan(4, 16, 2, 1, 0, 0)[0] == -1 and plan(4, 16, 2, 1, 10, -1)[0] == -1
+
+
+def test_workspace_holds_both_parts():
+    B, Hq, Hkv, Lq, Lp, Lk, d = 4, 16, 2, 2, 3000, 700, 64
+    np_, _ = plan(B, Hq, Hkv, Lq, Lp, 5)
+    ns, _ = ab.attn_decode_num_splits(B, Hq, Hkv, Lq, Lk, d)
+    rows = B * Hq * Lq
+    want = ((np_ + ns) * rows * d * 4 + 255) // 256 * 256 + (np_ + ns) * rows * 4
+    assert ab.attn_decode_shared_prefix_workspace_size(B, Hq, Hkv, Lq, Lp, Lk, d, 5) == want
+    with pytest.raises(ab.AttnError):
+        ab.attn_decode_shared_prefix_workspace_size(B, Hq, 3, Lq, Lp, Lk, d)
+
+
+def test_binding_rejects_host_tensors():
+    import torch
+    q = torch.zeros(1, 2, 1, 64, dtype=torch.bfloat16)
+    p = torch.zeros(2, 8, 64, dtype=torch.bfloat16)
+    k = torch.zeros(1, 2, 8, 64, dtype=torch.bfloat16)
+    kv = torch.ones(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        ab.attn_decode_shared_prefix(q, p, p, k, k, kv)
+    with pytest.raises(ValueError, match="CUDA"):
+        ab.attn_decode_shared_prefix_paged(q, k, k, kv, 8, kv.view(1, 1), kv)
