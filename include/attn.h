@@ -534,38 +534,59 @@ attn_status_t attn_cache_read_paged_q8(const void* k_pages, const void* v_pages,
                                        int pages_per_seq, int num_pages, int d, void* stream);
 
 /*
+ * attn_decode_q8_workspace_size — bytes of caller workspace the 8-bit decodes need
+ * (two partial results per CTA, whatever the batch and the lengths); 0 for invalid
+ * arguments.  num_ctas as below.
+ */
+size_t attn_decode_q8_workspace_size(int Hq, int Hkv, int Lq, int d, int num_ctas);
+
+/*
  * attn_decode_splitkv_q8 — attn_decode_splitkv over an 8-bit cache.
  *
  * Defines O and LSE of attn_decode_splitkv for the values the cache stands for:
  *   S_ij = scale * 2^(k_exp_j - 127) * <Q_i, kc_j>,  j in [0, kv_lens[b]),
  *   O_i = sum_j softmax_j(S_ij) 2^(v_exp_j - 127) vc_j,  LSE_i = log sum_j exp(S_ij).
- * The codes go to the tensor cores as exact f16 values; scores and sums are
- * fp32.  Codes and scale bytes at or past kv_lens[b] may hold anything.  A
- * sequence with kv_lens[b] = 0 gets O = 0 and LSE = -inf.
+ * The codes reach the tensor cores as exact 16-bit values; scores and sums are
+ * fp32.  Codes and scale bytes at or past kv_lens[b] may hold anything; a NaN code
+ * below it gives unspecified values in its sequence's rows.  A sequence with
+ * kv_lens[b] = 0 gets O = 0 and LSE = -inf.
+ *
+ * All sequences' key tiles are shared out evenly among num_ctas CTAs (0: one per SM
+ * of the current device; a smaller number leaves SMs to other streams), wherever
+ * the boundaries fall; two launches, the second merging the units that were cut.
+ * The result depends on num_ctas in its last bits only, and is the same from run to
+ * run.
  *
  * Arguments
- *   q, o, lse, kv_lens, B, Hq, Hkv, Lq, Lk_max, d, scale, num_splits, workspace,
- *   ws_bytes  as attn_decode_splitkv (the same split plan and workspace size)
+ *   q        [B, Hq, Lq, d] bf16, read
  *   k_cache, v_cache, k_exp, v_exp  the cache above, read below kv_lens[b]
- * Errors: as attn_decode_splitkv.
+ *   o        [B, Hq, Lq, d] bf16, written;  lse [B, Hq, Lq] fp32, written
+ *   kv_lens  [B] int32 DEVICE array, each in [0, Lk_max]; an entry outside is
+ *            clamped and flags the device error word
+ *   d in {64, 128}; scale > 0; Lk_max < 2^31 - 4096; 0 <= num_ctas <= 4096
+ *   workspace, ws_bytes  caller-owned device buffer, 256-byte aligned, at least
+ *            attn_decode_q8_workspace_size(...) bytes, not shared with a concurrent
+ *            call
+ * Errors: INVALID_ARG / UNSUPPORTED / WORKSPACE before any launch; CUDA on
+ * launch failure.
  */
 attn_status_t attn_decode_splitkv_q8(const void* q, const void* k_cache, const void* v_cache,
                                      const uint8_t* k_exp, const uint8_t* v_exp, void* o,
                                      float* lse, const int32_t* kv_lens, int B, int Hq, int Hkv,
-                                     int Lq, int Lk_max, int d, float scale, int num_splits,
+                                     int Lq, int Lk_max, int d, float scale, int num_ctas,
                                      void* workspace, size_t ws_bytes, void* stream);
 
 /*
- * attn_decode_paged_q8 — attn_decode_splitkv_q8 over pages; arguments and errors
- * as attn_decode_paged.  Block-table entries past a sequence's last page are
- * never read.
+ * attn_decode_paged_q8 — attn_decode_splitkv_q8 over pages (page sizes, block table
+ * and bad page ids as attn_decode_paged; Lk_max = pages_per_seq * page_size).
+ * Block-table entries past a sequence's last page are never read.
  */
 attn_status_t attn_decode_paged_q8(const void* q, const void* k_pages, const void* v_pages,
                                    const uint8_t* k_exp, const uint8_t* v_exp,
                                    const int32_t* block_table, void* o, float* lse,
                                    const int32_t* kv_lens, int B, int Hq, int Hkv, int Lq,
                                    int page_size, int pages_per_seq, int num_pages, int d,
-                                   float scale, int num_splits, void* workspace, size_t ws_bytes,
+                                   float scale, int num_ctas, void* workspace, size_t ws_bytes,
                                    void* stream);
 
 /*

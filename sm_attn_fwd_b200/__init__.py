@@ -40,6 +40,7 @@ __all__ = [
     "attn_decode_shared_prefix_num_splits", "attn_decode_shared_prefix_workspace_size",
     "attn_cache_append_q8", "attn_cache_append_paged_q8", "attn_cache_read_q8",
     "attn_cache_read_paged_q8", "attn_decode_splitkv_q8", "attn_decode_paged_q8",
+    "attn_decode_q8_workspace_size",
     "attn_get_device_error", "attn_selftest_wait_timeout", "attn_status_string",
     "EXPORTED_SYMBOLS",
 ]
@@ -70,6 +71,7 @@ EXPORTED_SYMBOLS = (
     "attn_decode_shared_prefix_num_splits", "attn_decode_shared_prefix_workspace_size",
     "attn_cache_append_q8", "attn_cache_append_paged_q8", "attn_cache_read_q8",
     "attn_cache_read_paged_q8", "attn_decode_splitkv_q8", "attn_decode_paged_q8",
+    "attn_decode_q8_workspace_size",
     "attn_get_device_error", "attn_selftest_wait_timeout", "attn_status_string",
 )
 
@@ -160,6 +162,8 @@ def load_library():
         lib.attn_cache_read_q8.restype = i32
         lib.attn_cache_read_paged_q8.argtypes = [P] * 8 + [i32] * 6 + [P]
         lib.attn_cache_read_paged_q8.restype = i32
+        lib.attn_decode_q8_workspace_size.argtypes = [i32] * 5
+        lib.attn_decode_q8_workspace_size.restype = sz
         lib.attn_decode_splitkv_q8.argtypes = [P] * 8 + [i32] * 6 + [f32, i32, P, sz, P]
         lib.attn_decode_splitkv_q8.restype = i32
         lib.attn_decode_paged_q8.argtypes = [P] * 9 + [i32] * 8 + [f32, i32, P, sz, P]
@@ -576,20 +580,30 @@ def attn_decode_splitkv_noalloc(q, k_cache, v_cache, kv_lens, *, scale=None, num
     return o, lse
 
 
-def _check(name, t, dtype, shape, device):
-    """t must be a contiguous CUDA tensor of this type and shape on ``device``."""
+def _check(name, t, dtype, shape, index):
+    """t must be a contiguous CUDA tensor of this type and shape on CUDA device ``index``."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == index and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                     f"got {t.dtype} {tuple(t.shape)}")
 
 
-def _on(device):
-    """The library launches on the current device: make it the tensors' device."""
-    return torch.cuda.device(device)
+def _call(where, fn, index, stream, args):
+    """fn(*args, stream) on CUDA device ``index`` (the library launches on the current
+    device, so it is made that one); raises AttnError unless it returns ATTN_OK."""
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _call(where, fn, index, stream, args)
+    if stream is None:
+        stream = torch.cuda.current_stream(index)
+    st = fn(*args, stream.cuda_stream)
+    if st != ATTN_OK:
+        raise AttnError(st, where)
 
 
 def _cache_shape(k_cache, block_table):
@@ -609,14 +623,46 @@ def _cache_shape(k_cache, block_table):
 
 
 def _check_q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, B):
-    dev = k_cache.device
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check(name, t, torch.float8_e4m3fn, k_cache.shape, dev)
-    for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
-        _check(name, t, torch.uint8, k_cache.shape[:3], dev)
+    """Checks the tensors of an 8-bit cache; returns their CUDA device's index."""
+    shape = k_cache.shape
+    dev = k_cache.get_device()
+    _check("k_cache", k_cache, torch.float8_e4m3fn, shape, dev)
+    _check("v_cache", v_cache, torch.float8_e4m3fn, shape, dev)
+    _check("k_exp", k_exp, torch.uint8, shape[:3], dev)
+    _check("v_exp", v_exp, torch.uint8, shape[:3], dev)
     if block_table is not None:
         _check("block_table", block_table, torch.int32, block_table.shape, dev)
     _check("kv_lens", kv_lens, torch.int32, (B,), dev)
+    return dev
+
+
+def _check_decode(q, B, d, scale, o, lse, dev):
+    """Checks a decode's queries and outputs (allocated when None): (Hq, Lq, scale, o, lse)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a [B, Hq, Lq, d] CUDA tensor")
+    _, Hq, Lq, _ = q.shape
+    _check("q", q, torch.bfloat16, (B, Hq, Lq, d), dev)
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _check("o", o, torch.bfloat16, q.shape, dev)
+    if lse is None:
+        lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
+    else:
+        _check("lse", lse, torch.float32, (B, Hq, Lq), dev)
+    return Hq, Lq, 1.0 / math.sqrt(d) if scale is None else float(scale), o, lse
+
+
+def _workspace(workspace, need, q, where):
+    """(pointer, bytes) of a workspace, allocated with ``need`` bytes when not given."""
+    if workspace is None:
+        if need == 0:
+            raise AttnError(ATTN_ERR_INVALID_ARG, where)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif (not isinstance(workspace, torch.Tensor) or workspace.get_device() != q.get_device()
+            or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {q.device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def attn_decode_shared_prefix_num_splits(B, Hq, Hkv, Lq, Lp, num_splits=0):
@@ -646,13 +692,27 @@ def attn_decode_shared_prefix(q, k_prefix, v_prefix, k_cache, v_cache, kv_lens, 
     k_cache/v_cache: [B, Hkv, Lk_max, d], the sequences' own keys; kv_lens: [B] int32,
     how many of those each has (0 allowed).  Returns (o, lse).
     """
+    B, Hkv, Lk, d, _, _, _ = _cache_shape(k_cache, None)
     if not isinstance(k_prefix, torch.Tensor) or k_prefix.dim() != 3:
         raise ValueError("k_prefix must be a [Hkv, Lp, d] CUDA tensor")
-    B, Hkv, Lk, d, _, _, _ = _cache_shape(k_cache, None)
+    Lp = k_prefix.shape[1]
+    dev = k_cache.get_device()
     for name, t in (("k_prefix", k_prefix), ("v_prefix", v_prefix)):
-        _check(name, t, torch.bfloat16, (Hkv, k_prefix.shape[1], d), k_cache.device)
-    return _shared_prefix(q, k_prefix, v_prefix, None, k_prefix.shape[1], k_cache, v_cache, None,
-                          kv_lens, scale, num_splits, workspace, o, lse, stream)
+        _check(name, t, torch.bfloat16, (Hkv, Lp, d), dev)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check(name, t, torch.bfloat16, (B, Hkv, Lk, d), dev)
+    _check("kv_lens", kv_lens, torch.int32, (B,), dev)
+    Hq, Lq, scale, o, lse = _check_decode(q, B, d, scale, o, lse, dev)
+    lib = _lib or load_library()
+    where = "attn_decode_shared_prefix"
+    need = 0 if workspace is not None else lib.attn_decode_shared_prefix_workspace_size(
+        B, Hq, Hkv, Lq, Lp, Lk, d, num_splits)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, need, q, where)
+    _call(where, lib.attn_decode_shared_prefix, dev, stream,
+          (q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(),
+           v_cache.data_ptr(), o.data_ptr(), lse.data_ptr(), kv_lens.data_ptr(), B, Hq, Hkv, Lq,
+           Lp, Lk, d, scale, int(num_splits), ws_ptr, ws_bytes))
+    return o, lse
 
 
 def attn_decode_shared_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len, block_table,
@@ -667,53 +727,24 @@ def attn_decode_shared_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_le
     """
     if block_table is None:
         raise ValueError("block_table must be an int32 CUDA tensor [B, pages_per_seq]")
-    page = _cache_shape(k_pages, block_table)[4]
-    _check("prefix_table", prefix_table, torch.int32, (-(-int(prefix_len) // max(page, 1)),),
-           k_pages.device)
-    return _shared_prefix(q, None, None, prefix_table, int(prefix_len), k_pages, v_pages,
-                          block_table, kv_lens, scale, num_splits, workspace, o, lse, stream)
-
-
-def _shared_prefix(q, k_prefix, v_prefix, prefix_table, Lp, k_cache, v_cache, block_table, kv_lens,
-                   scale, num_splits, workspace, o, lse, stream):
-    B, Hkv, Lk, d, page, per_seq, n_pages = _cache_shape(k_cache, block_table)
-    dev = k_cache.device
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check(name, t, torch.bfloat16, k_cache.shape, dev)
-    if block_table is not None:
-        _check("block_table", block_table, torch.int32, block_table.shape, dev)
+    B, Hkv, Lk, d, page, per_seq, n_pages = _cache_shape(k_pages, block_table)
+    Lp = int(prefix_len)
+    dev = k_pages.get_device()
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _check(name, t, torch.bfloat16, k_pages.shape, dev)
+    _check("prefix_table", prefix_table, torch.int32, (-(-Lp // max(page, 1)),), dev)
+    _check("block_table", block_table, torch.int32, (B, per_seq), dev)
     _check("kv_lens", kv_lens, torch.int32, (B,), dev)
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be a [B, Hq, Lq, d] CUDA tensor")
-    _, Hq, Lq, _ = q.shape
-    _check("q", q, torch.bfloat16, (B, Hq, Lq, d), dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    o = torch.empty_like(q) if o is None else o
-    _check("o", o, torch.bfloat16, q.shape, dev)
-    if lse is None:
-        lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=dev)
-    _check("lse", lse, torch.float32, (B, Hq, Lq), dev)
-    lib = load_library()
-    with _on(dev):
-        if workspace is None:
-            need = attn_decode_shared_prefix_workspace_size(B, Hq, Hkv, Lq, Lp, Lk, d, num_splits)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        tail = (float(scale), int(num_splits), _ptr(workspace),
-                workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
-        if block_table is None:
-            name = "attn_decode_shared_prefix"
-            st = lib.attn_decode_shared_prefix(
-                _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k_cache), _ptr(v_cache), _ptr(o),
-                _ptr(lse), _ptr(kv_lens), B, Hq, Hkv, Lq, Lp, Lk, d, *tail)
-        else:
-            name = "attn_decode_shared_prefix_paged"
-            st = lib.attn_decode_shared_prefix_paged(
-                _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_table), _ptr(block_table),
-                _ptr(o), _ptr(lse), _ptr(kv_lens), B, Hq, Hkv, Lq, Lp, page, per_seq, n_pages, d,
-                *tail)
-    if st != ATTN_OK:
-        raise AttnError(st, name)
+    Hq, Lq, scale, o, lse = _check_decode(q, B, d, scale, o, lse, dev)
+    lib = _lib or load_library()
+    where = "attn_decode_shared_prefix_paged"
+    need = 0 if workspace is not None else lib.attn_decode_shared_prefix_workspace_size(
+        B, Hq, Hkv, Lq, Lp, Lk, d, num_splits)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, need, q, where)
+    _call(where, lib.attn_decode_shared_prefix_paged, dev, stream,
+          (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), prefix_table.data_ptr(),
+           block_table.data_ptr(), o.data_ptr(), lse.data_ptr(), kv_lens.data_ptr(), B, Hq, Hkv,
+           Lq, Lp, page, per_seq, n_pages, d, scale, int(num_splits), ws_ptr, ws_bytes))
     return o, lse
 
 
@@ -743,29 +774,25 @@ def attn_cache_append_paged_q8(k, v, k_pages, v_pages, k_exp, v_exp, block_table
 
 def _cache_append(k, v, k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, new_lens, stream):
     B, Hkv, Lk, d, page, per_seq, n_pages = _cache_shape(k_cache, block_table)
-    _check_q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, B)
-    dev = k_cache.device
+    dev = _check_q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, B)
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be a [B, Hkv, Ln, d] CUDA tensor")
     Ln = k.shape[2]
-    for name, t in (("k", k), ("v", v)):
-        _check(name, t, torch.bfloat16, (B, Hkv, Ln, d), dev)
+    _check("k", k, torch.bfloat16, (B, Hkv, Ln, d), dev)
+    _check("v", v, torch.bfloat16, (B, Hkv, Ln, d), dev)
     if new_lens is not None:
         _check("new_lens", new_lens, torch.int32, (B,), dev)
-    head = (_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(k_exp), _ptr(v_exp))
-    with _on(dev):
-        if block_table is None:
-            name = "attn_cache_append_q8"
-            st = load_library().attn_cache_append_q8(
-                *head, _ptr(kv_lens), _ptr(new_lens), B, Hkv, Ln, Lk, d,
-                _stream_handle(stream, dev))
-        else:
-            name = "attn_cache_append_paged_q8"
-            st = load_library().attn_cache_append_paged_q8(
-                *head, _ptr(block_table), _ptr(kv_lens), _ptr(new_lens), B, Hkv, Ln, page, per_seq,
-                n_pages, d, _stream_handle(stream, dev))
-    if st != ATTN_OK:
-        raise AttnError(st, name)
+        new_lens = new_lens.data_ptr()
+    lib = _lib or load_library()
+    head = (k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(),
+            v_exp.data_ptr())
+    if block_table is None:
+        _call("attn_cache_append_q8", lib.attn_cache_append_q8, dev, stream,
+              head + (kv_lens.data_ptr(), new_lens, B, Hkv, Ln, Lk, d))
+    else:
+        _call("attn_cache_append_paged_q8", lib.attn_cache_append_paged_q8, dev, stream,
+              head + (block_table.data_ptr(), kv_lens.data_ptr(), new_lens, B, Hkv, Ln, page,
+                      per_seq, n_pages, d))
 
 
 def attn_cache_read_q8(k_cache, v_cache, k_exp, v_exp, kv_lens, *, k=None, v=None, stream=None):
@@ -786,87 +813,75 @@ def attn_cache_read_paged_q8(k_pages, v_pages, k_exp, v_exp, block_table, kv_len
 
 def _cache_read(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, k, v, stream):
     B, Hkv, Lk, d, page, per_seq, n_pages = _cache_shape(k_cache, block_table)
-    _check_q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, B)
-    dev = k_cache.device
+    dev = _check_q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, B)
     shape = (B, Hkv, Lk, d)
-    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
-    for name, t in (("k", k), ("v", v)):
-        _check(name, t, torch.bfloat16, shape, dev)
-    head = (_ptr(k_cache), _ptr(v_cache), _ptr(k_exp), _ptr(v_exp))
-    with _on(dev):
-        if block_table is None:
-            name = "attn_cache_read_q8"
-            st = load_library().attn_cache_read_q8(
-                *head, _ptr(kv_lens), _ptr(k), _ptr(v), B, Hkv, Lk, d, _stream_handle(stream, dev))
-        else:
-            name = "attn_cache_read_paged_q8"
-            st = load_library().attn_cache_read_paged_q8(
-                *head, _ptr(block_table), _ptr(kv_lens), _ptr(k), _ptr(v), B, Hkv, page, per_seq,
-                n_pages, d, _stream_handle(stream, dev))
-    if st != ATTN_OK:
-        raise AttnError(st, name)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) if v is None else v
+    _check("k", k, torch.bfloat16, shape, dev)
+    _check("v", v, torch.bfloat16, shape, dev)
+    lib = _lib or load_library()
+    head = (k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr())
+    if block_table is None:
+        _call("attn_cache_read_q8", lib.attn_cache_read_q8, dev, stream,
+              head + (kv_lens.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hkv, Lk, d))
+    else:
+        _call("attn_cache_read_paged_q8", lib.attn_cache_read_paged_q8, dev, stream,
+              head + (block_table.data_ptr(), kv_lens.data_ptr(), k.data_ptr(), v.data_ptr(), B,
+                      Hkv, page, per_seq, n_pages, d))
     return k, v
 
 
+def attn_decode_q8_workspace_size(Hq, Hkv, Lq, d, num_ctas=0) -> int:
+    n = load_library().attn_decode_q8_workspace_size(Hq, Hkv, Lq, d, num_ctas)
+    if n == 0:
+        raise AttnError(ATTN_ERR_INVALID_ARG, "attn_decode_q8_workspace_size")
+    return int(n)
+
+
 def attn_decode_splitkv_q8(q, k_cache, v_cache, k_exp, v_exp, kv_lens, *, scale=None,
-                           num_splits=0, workspace=None, o=None, lse=None, stream=None):
+                           num_ctas=0, workspace=None, o=None, lse=None, stream=None):
     """Split-KV decode over an 8-bit cache (see ``attn_decode_splitkv_q8`` in
     include/attn.h).
 
     q: [B, Hq, Lq, d] bf16; the cache as for ``attn_cache_append_q8``; kv_lens: [B]
-    int32.  ``workspace`` (uint8, attn_decode_workspace_size bytes) is allocated here
-    when not given.  Returns (o, lse).
+    int32.  num_ctas: how many CTAs share the work (0: one per SM).  ``workspace``
+    (uint8, attn_decode_q8_workspace_size bytes) is allocated here when not given.
+    Returns (o, lse).
     """
-    return _decode_q8(q, k_cache, v_cache, k_exp, v_exp, None, kv_lens, scale, num_splits,
+    return _decode_q8(q, k_cache, v_cache, k_exp, v_exp, None, kv_lens, scale, num_ctas,
                       workspace, o, lse, stream)
 
 
 def attn_decode_paged_q8(q, k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, *, scale=None,
-                         num_splits=0, workspace=None, o=None, lse=None, stream=None):
+                         num_ctas=0, workspace=None, o=None, lse=None, stream=None):
     """attn_decode_splitkv_q8 over pages (see ``attn_decode_paged_q8`` in
     include/attn.h); the cache as for ``attn_cache_append_paged_q8``."""
     if block_table is None:
         raise ValueError("block_table must be an int32 CUDA tensor [B, pages_per_seq]")
-    return _decode_q8(q, k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, scale, num_splits,
+    return _decode_q8(q, k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, scale, num_ctas,
                       workspace, o, lse, stream)
 
 
-def _decode_q8(q, k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, scale, num_splits,
+def _decode_q8(q, k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, scale, num_ctas,
                workspace, o, lse, stream):
     B, Hkv, Lk, d, page, per_seq, n_pages = _cache_shape(k_cache, block_table)
-    _check_q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, B)
-    dev = k_cache.device
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be a [B, Hq, Lq, d] CUDA tensor")
-    _, Hq, Lq, _ = q.shape
-    _check("q", q, torch.bfloat16, (B, Hq, Lq, d), dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    o = torch.empty_like(q) if o is None else o
-    _check("o", o, torch.bfloat16, q.shape, dev)
-    if lse is None:
-        lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=dev)
-    _check("lse", lse, torch.float32, (B, Hq, Lq), dev)
-    head = (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_exp), _ptr(v_exp))
-    lib = load_library()
-    with _on(dev):
-        if workspace is None:
-            need = attn_decode_workspace_size(B, Hq, Hkv, Lq, Lk, d, num_splits)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        tail = (float(scale), int(num_splits), _ptr(workspace),
-                workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
-        if block_table is None:
-            name = "attn_decode_splitkv_q8"
-            st = lib.attn_decode_splitkv_q8(*head, _ptr(o), _ptr(lse), _ptr(kv_lens), B, Hq, Hkv,
-                                            Lq, Lk, d, *tail)
-        else:
-            name = "attn_decode_paged_q8"
-            st = lib.attn_decode_paged_q8(*head, _ptr(block_table), _ptr(o), _ptr(lse),
-                                          _ptr(kv_lens), B, Hq, Hkv, Lq, page, per_seq, n_pages, d,
-                                          *tail)
-    if st != ATTN_OK:
-        raise AttnError(st, name)
+    dev = _check_q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, B)
+    Hq, Lq, scale, o, lse = _check_decode(q, B, d, scale, o, lse, dev)
+    lib = _lib or load_library()
+    where = "attn_decode_splitkv_q8" if block_table is None else "attn_decode_paged_q8"
+    need = 0 if workspace is not None else lib.attn_decode_q8_workspace_size(Hq, Hkv, Lq, d,
+                                                                             num_ctas)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, need, q, where)
+    head = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(),
+            v_exp.data_ptr())
+    tail = (d, scale, int(num_ctas), ws_ptr, ws_bytes)
+    if block_table is None:
+        _call(where, lib.attn_decode_splitkv_q8, dev, stream,
+              head + (o.data_ptr(), lse.data_ptr(), kv_lens.data_ptr(), B, Hq, Hkv, Lq, Lk) + tail)
+    else:
+        _call(where, lib.attn_decode_paged_q8, dev, stream,
+              head + (block_table.data_ptr(), o.data_ptr(), lse.data_ptr(), kv_lens.data_ptr(), B,
+                      Hq, Hkv, Lq, page, per_seq, n_pages) + tail)
     return o, lse
 
 

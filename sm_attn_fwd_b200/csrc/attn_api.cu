@@ -46,6 +46,11 @@ cudaError_t launch_decode_q8(const CUtensorMap&, const CUtensorMap&, const Decod
                              cudaStream_t);
 int decode_q8_box_rows(int page_size);
 template <int D>
+cudaError_t launch_decode_q8_wide(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                                  const DecodeQ8Params&, cudaStream_t);
+template <int D>
+cudaError_t launch_decode_q8_combine(const DecodeQ8Params&, cudaStream_t);
+template <int D>
 cudaError_t launch_prefix(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
                           const PrefixParams&, cudaStream_t);
 }  // namespace attn
@@ -116,7 +121,7 @@ struct TmapKey {
            dim3 == o.dim3;
   }
 };
-constexpr int kTmapCacheSize = 16;
+constexpr int kTmapCacheSize = 64;
 struct TmapCache {
   TmapKey key[kTmapCacheSize];
   CUtensorMap map[kTmapCacheSize];
@@ -1335,10 +1340,34 @@ attn_status_t read_impl(const void* k_codes, const void* v_codes, const uint8_t*
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+// CTAs of the 8-bit decode (one per SM unless the caller asks for a number), and its
+// workspace: two partial results per CTA.
+constexpr int kMaxQ8Ctas = 4096;
+
+struct Q8Plan {
+  int num_ctas, tile_rows, row_tiles;
+  size_t lse_off, bytes;
+};
+
+bool plan_q8(int Hq, int Hkv, int Lq, int d, int num_ctas, Q8Plan* pl) {
+  if (Hq < 1 || Hkv < 1 || Lq < 1 || d < 1 || Hq % Hkv) return false;
+  if (num_ctas < 0 || num_ctas > kMaxQ8Ctas) return false;
+  const long long rows = (long long)(Hq / Hkv) * Lq;
+  pl->num_ctas = num_ctas > 0 ? num_ctas : num_sms();
+  pl->tile_rows = attn::decode_q8_tile_rows(d, rows);
+  const long long tiles = ceil_div(rows, pl->tile_rows);
+  if (tiles * Hkv > 0x7fffffffLL) return false;
+  pl->row_tiles = (int)tiles;
+  const size_t part_rows = 2 * (size_t)pl->num_ctas * (size_t)pl->tile_rows;
+  pl->lse_off = (part_rows * (size_t)d * 4 + 255) / 256 * 256;
+  pl->bytes = pl->lse_off + part_rows * 4;
+  return true;
+}
+
 attn_status_t decode_q8_impl(const void* q, const void* k_codes, const void* v_codes,
                              const uint8_t* k_exp, const uint8_t* v_exp, void* o, float* lse,
                              const int32_t* kv_lens, int B, int Hq, int Hkv, int Lq, int Lk_max,
-                             int d, float scale, int num_splits, void* workspace, size_t ws_bytes,
+                             int d, float scale, int num_ctas, void* workspace, size_t ws_bytes,
                              void* stream, const PagedKv& pg) {
   if (!q || !k_codes || !v_codes || !k_exp || !v_exp || !o || !lse || !kv_lens)
     return ATTN_ERR_INVALID_ARG;
@@ -1346,13 +1375,13 @@ attn_status_t decode_q8_impl(const void* q, const void* k_codes, const void* v_c
       !aligned(lse, 4) || !aligned(kv_lens, 4))
     return ATTN_ERR_INVALID_ARG;
   if (!(scale > 0.0f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
-  SplitPlan pl;
-  if (!plan_splits(B, Hq, Hkv, Lq, Lk_max, d, num_splits, &pl)) return ATTN_ERR_INVALID_ARG;
+  Q8Plan pl;
+  if (B < 1 || Lk_max < 1 || !plan_q8(Hq, Hkv, Lq, d, num_ctas, &pl)) return ATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (Lk_max > 0x7fffffff - 4096) return ATTN_ERR_UNSUPPORTED;  // key counters are 32-bit
   if ((long long)B * Hq > 0x7fffffffLL / Lq) return ATTN_ERR_UNSUPPORTED;
   const long long nrows = (long long)B * Hq * Lq;
-  const size_t need = attn_decode_workspace_size(B, Hq, Hkv, Lq, Lk_max, d, num_splits);
-  if (!workspace || !aligned(workspace, 256) || ws_bytes < need) return ATTN_ERR_WORKSPACE;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < pl.bytes) return ATTN_ERR_WORKSPACE;
 
   attn::DecodeQ8Params p;
   std::memset(&p, 0, sizeof p);
@@ -1360,8 +1389,7 @@ attn_status_t decode_q8_impl(const void* q, const void* k_codes, const void* v_c
   p.o = o;
   p.lse = lse;
   p.ws_o = reinterpret_cast<float*>(workspace);
-  p.ws_lse = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) +
-                                      ws_lse_offset(pl, nrows, d));
+  p.ws_lse = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + pl.lse_off);
   p.k_exp = k_exp;
   p.v_exp = v_exp;
   p.kv_lens = kv_lens;
@@ -1373,8 +1401,9 @@ attn_status_t decode_q8_impl(const void* q, const void* k_codes, const void* v_c
   p.Lk = Lk_max;
   p.group = Hq / Hkv;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634074);
-  p.chunk = pl.chunk;
-  p.nsplit = pl.nsplit;
+  p.num_ctas = pl.num_ctas;
+  p.tile_rows = pl.tile_rows;
+  p.row_tiles = pl.row_tiles;
   p.page_size = pg.page_size;
   p.page_shift = pg.block_table ? log2_of(pg.page_size) : 0;
   p.pages_per_seq = pg.pages_per_seq;
@@ -1387,26 +1416,26 @@ attn_status_t decode_q8_impl(const void* q, const void* k_codes, const void* v_c
   const uint64_t planes =
       pg.block_table ? (uint64_t)pg.num_pages * (uint64_t)Hkv : (uint64_t)B * (uint64_t)Hkv;
   const uint64_t dims[3] = {(uint64_t)d, rows, planes};
-  const int box = attn::decode_q8_box_rows(pg.block_table ? pg.page_size : 1 << 16);
+  const bool wide = pl.tile_rows == kBlockM;
+  const int page_rows = pg.block_table ? pg.page_size : 1 << 16;
+  const int box = wide ? std::min(page_rows, 64) : attn::decode_q8_box_rows(page_rows);
   if (!encode_codes(&tk, k_codes, dims, box) || !encode_codes(&tv, v_codes, dims, box))
     return ATTN_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = d == 64 ? attn::launch_decode_q8<64>(tk, tv, p, st)
-                          : attn::launch_decode_q8<128>(tk, tv, p, st);
+  cudaError_t e;
+  if (wide) {
+    CUtensorMap tq;
+    const uint64_t dq[2] = {(uint64_t)d, (uint64_t)nrows};
+    if (!encode_bf16(&tq, q, 2, dq)) return ATTN_ERR_CUDA;
+    e = d == 64 ? attn::launch_decode_q8_wide<64>(tq, tk, tv, p, st)
+                : attn::launch_decode_q8_wide<128>(tq, tk, tv, p, st);
+  } else {
+    e = d == 64 ? attn::launch_decode_q8<64>(tk, tv, p, st)
+                : attn::launch_decode_q8<128>(tk, tv, p, st);
+  }
   if (e != cudaSuccess) return ATTN_ERR_CUDA;
-  if (pl.nsplit == 1) return ATTN_OK;  // the only split wrote O and the LSE
-
-  FwdParams c;
-  std::memset(&c, 0, sizeof c);
-  c.o = o;
-  c.lse = lse;
-  c.ws_o = p.ws_o;
-  c.ws_lse = p.ws_lse;
-  c.B = B;
-  c.Hq = Hq;
-  c.Lq = Lq;
-  c.nsplit = pl.nsplit;
-  e = d == 64 ? attn::launch_combine<64>(c, st) : attn::launch_combine<128>(c, st);
+  e = d == 64 ? attn::launch_decode_q8_combine<64>(p, st)
+              : attn::launch_decode_q8_combine<128>(p, st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -1457,13 +1486,18 @@ attn_status_t attn_cache_read_paged_q8(const void* k_pages, const void* v_pages,
   return read_impl(k_pages, v_pages, k_exp, v_exp, kv_lens, k, v, B, Hkv, lk, d, pg, stream);
 }
 
+size_t attn_decode_q8_workspace_size(int Hq, int Hkv, int Lq, int d, int num_ctas) {
+  Q8Plan pl;
+  return plan_q8(Hq, Hkv, Lq, d, num_ctas, &pl) ? pl.bytes : 0;
+}
+
 attn_status_t attn_decode_splitkv_q8(const void* q, const void* k_cache, const void* v_cache,
                                      const uint8_t* k_exp, const uint8_t* v_exp, void* o,
                                      float* lse, const int32_t* kv_lens, int B, int Hq, int Hkv,
-                                     int Lq, int Lk_max, int d, float scale, int num_splits,
+                                     int Lq, int Lk_max, int d, float scale, int num_ctas,
                                      void* workspace, size_t ws_bytes, void* stream) {
   return decode_q8_impl(q, k_cache, v_cache, k_exp, v_exp, o, lse, kv_lens, B, Hq, Hkv, Lq,
-                        Lk_max, d, scale, num_splits, workspace, ws_bytes, stream, PagedKv{});
+                        Lk_max, d, scale, num_ctas, workspace, ws_bytes, stream, PagedKv{});
 }
 
 attn_status_t attn_decode_paged_q8(const void* q, const void* k_pages, const void* v_pages,
@@ -1471,7 +1505,7 @@ attn_status_t attn_decode_paged_q8(const void* q, const void* k_pages, const voi
                                    const int32_t* block_table, void* o, float* lse,
                                    const int32_t* kv_lens, int B, int Hq, int Hkv, int Lq,
                                    int page_size, int pages_per_seq, int num_pages, int d,
-                                   float scale, int num_splits, void* workspace, size_t ws_bytes,
+                                   float scale, int num_ctas, void* workspace, size_t ws_bytes,
                                    void* stream) {
   PagedKv pg;
   int lk = 0;
@@ -1479,7 +1513,7 @@ attn_status_t attn_decode_paged_q8(const void* q, const void* k_pages, const voi
       parse_paged(block_table, Hkv, page_size, pages_per_seq, num_pages, &pg, &lk);
   if (st != ATTN_OK) return st;
   return decode_q8_impl(q, k_pages, v_pages, k_exp, v_exp, o, lse, kv_lens, B, Hq, Hkv, Lq, lk, d,
-                        scale, num_splits, workspace, ws_bytes, stream, pg);
+                        scale, num_ctas, workspace, ws_bytes, stream, pg);
 }
 
 }  // extern "C"

@@ -64,41 +64,49 @@ __device__ __forceinline__ uint2 quantise8(const uint4& raw, int& e_out) {
   return c;
 }
 
-template <int D>
+// U rows per lane group, kCacheThreads / kLanes rows apart: their loads go out together.
+template <int D, int U>
 __global__ void __launch_bounds__(kCacheThreads) attn_cache_append_kernel(const CacheParams p) {
   constexpr int kLanes = D / 8;
-  const long long idx = (long long)blockIdx.x * kCacheThreads + threadIdx.x;
+  constexpr int kGroups = kCacheThreads / kLanes;  // rows a block takes at a time
   const int part = threadIdx.x % kLanes;
   const int nrows = p.B * p.Hkv * p.Ln;  // at most 2^31 - 1, checked on the host
-  const long long row_l = idx / kLanes;
-  bool live = row_l < nrows;
-  const int row = live ? (int)row_l : 0;
-  const int bh = row / p.Ln, i = row - bh * p.Ln;
-  const int b = bh / p.Hkv, h = bh - b * p.Hkv;
-  // every lane stays for the shuffles; a lane group is live as a whole
-  const int len = __ldg(p.kv_lens + b);
-  const int n_new = p.new_lens ? __ldg(p.new_lens + b) : p.Ln;
-  if (len < 0 || len > p.Lk || n_new < 0 || n_new > p.Ln || n_new > len) {
-    if (live && i == 0 && h == 0 && part == 0) atomicOr(p.err, kDevErrBadKvLen);
-    live = false;
-  }
-  live = live && i < n_new;
-  uint4 kr = make_uint4(0, 0, 0, 0), vr = kr;
-  if (live) {
+  const long long first = (long long)blockIdx.x * (kGroups * U) + threadIdx.x / kLanes;
+  uint4 kr[U], vr[U];
+  long long dst[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    kr[u] = vr[u] = make_uint4(0, 0, 0, 0);
+    dst[u] = -1;
+    if (first + u * kGroups >= nrows) continue;
+    const int row = (int)(first + u * kGroups);
+    const int bh = row / p.Ln, i = row - bh * p.Ln;
+    const int b = bh / p.Hkv, h = bh - b * p.Hkv;
+    const int len = __ldg(p.kv_lens + b);
+    const int n_new = p.new_lens ? __ldg(p.new_lens + b) : p.Ln;
+    if (len < 0 || len > p.Lk || n_new < 0 || n_new > p.Ln || n_new > len) {
+      if (i == 0 && h == 0 && part == 0) atomicOr(p.err, kDevErrBadKvLen);
+      continue;
+    }
+    if (i >= n_new) continue;
     const long long at = (long long)row * kLanes + part;  // in 16-byte units
-    kr = __ldcs(reinterpret_cast<const uint4*>(p.k_in) + at);
-    vr = __ldcs(reinterpret_cast<const uint4*>(p.v_in) + at);
+    kr[u] = __ldcs(reinterpret_cast<const uint4*>(p.k_in) + at);
+    vr[u] = __ldcs(reinterpret_cast<const uint4*>(p.v_in) + at);
+    dst[u] = cache_row(p, b, h, len - n_new + i);
   }
-  const long long dst = live ? cache_row(p, b, h, len - n_new + i) : -1;
-  int ek, ev;
-  const uint2 kc = quantise8<kLanes>(kr, ek);
-  const uint2 vc = quantise8<kLanes>(vr, ev);
-  if (dst >= 0) {
-    reinterpret_cast<uint2*>(p.k_codes)[dst * kLanes + part] = kc;
-    reinterpret_cast<uint2*>(p.v_codes)[dst * kLanes + part] = vc;
-    if (part == 0) {
-      p.k_exp[dst] = (uint8_t)ek;
-      p.v_exp[dst] = (uint8_t)ev;
+  // every lane takes part in the shuffles; a lane group is live as a whole
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    int ek, ev;
+    const uint2 kc = quantise8<kLanes>(kr[u], ek);
+    const uint2 vc = quantise8<kLanes>(vr[u], ev);
+    if (dst[u] >= 0) {
+      reinterpret_cast<uint2*>(p.k_codes)[dst[u] * kLanes + part] = kc;
+      reinterpret_cast<uint2*>(p.v_codes)[dst[u] * kLanes + part] = vc;
+      if (part == 0) {
+        p.k_exp[dst[u]] = (uint8_t)ek;
+        p.v_exp[dst[u]] = (uint8_t)ev;
+      }
     }
   }
 }
@@ -122,57 +130,85 @@ __device__ __forceinline__ void restore16(const uint4& c, float s, uint4 (&out)[
   out[1] = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-template <int D>
+template <int D, int U>
 __global__ void __launch_bounds__(kCacheThreads) attn_cache_read_kernel(const CacheParams p) {
   constexpr int kLanes = D / 16;
-  const long long idx = (long long)blockIdx.x * kCacheThreads + threadIdx.x;
+  constexpr int kGroups = kCacheThreads / kLanes;
   const int part = threadIdx.x % kLanes;
   const int nrows = p.B * p.Hkv * p.Lk;
-  if (idx / kLanes >= nrows) return;
-  const int row = (int)(idx / kLanes);
-  const int bh = row / p.Lk, j = row - bh * p.Lk;
-  const int b = bh / p.Hkv, h = bh - b * p.Hkv;
-  int len = __ldg(p.kv_lens + b);
-  if (len < 0 || len > p.Lk) {
-    if (j == 0 && h == 0 && part == 0) atomicOr(p.err, kDevErrBadKvLen);
-    return;
-  }
-  if (j >= len) return;
-  const long long src = cache_row(p, b, h, j);
-  uint4 ko[2], vo[2];
-  if (src >= 0) {
-    const uint4 kc = __ldcs(reinterpret_cast<const uint4*>(p.k_codes) + src * kLanes + part);
-    const uint4 vc = __ldcs(reinterpret_cast<const uint4*>(p.v_codes) + src * kLanes + part);
-    restore16(kc, q8::scale_of(p.k_exp[src]), ko);
-    restore16(vc, q8::scale_of(p.v_exp[src]), vo);
-  } else {
-    ko[0] = ko[1] = vo[0] = vo[1] = make_uint4(0, 0, 0, 0);
-  }
-  const long long dst = ((long long)row * kLanes + part) * 2;
+  const long long first = (long long)blockIdx.x * (kGroups * U) + threadIdx.x / kLanes;
+  uint4 kc[U], vc[U];
+  float ks[U], vs[U];
+  bool live[U];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    reinterpret_cast<uint4*>(p.k_out)[dst + i] = ko[i];
-    reinterpret_cast<uint4*>(p.v_out)[dst + i] = vo[i];
+  for (int u = 0; u < U; ++u) {
+    kc[u] = vc[u] = make_uint4(0, 0, 0, 0);
+    ks[u] = vs[u] = 0.0f;
+    live[u] = false;
+    if (first + u * kGroups >= nrows) continue;
+    const int row = (int)(first + u * kGroups);
+    const int bh = row / p.Lk, j = row - bh * p.Lk;
+    const int b = bh / p.Hkv, h = bh - b * p.Hkv;
+    const int len = __ldg(p.kv_lens + b);
+    if (len < 0 || len > p.Lk) {
+      if (j == 0 && h == 0 && part == 0) atomicOr(p.err, kDevErrBadKvLen);
+      continue;
+    }
+    if (j >= len) continue;
+    live[u] = true;
+    const long long src = cache_row(p, b, h, j);
+    if (src < 0) continue;  // reads as zeros
+    kc[u] = __ldcs(reinterpret_cast<const uint4*>(p.k_codes) + src * kLanes + part);
+    vc[u] = __ldcs(reinterpret_cast<const uint4*>(p.v_codes) + src * kLanes + part);
+    ks[u] = q8::scale_of(__ldg(p.k_exp + src));
+    vs[u] = q8::scale_of(__ldg(p.v_exp + src));
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (!live[u]) continue;
+    uint4 ko[2], vo[2];
+    restore16(kc[u], ks[u], ko);
+    restore16(vc[u], vs[u], vo);
+    const long long dst = ((first + u * kGroups) * kLanes + part) * 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      __stcs(reinterpret_cast<uint4*>(p.k_out) + dst + i, ko[i]);
+      __stcs(reinterpret_cast<uint4*>(p.v_out) + dst + i, vo[i]);
+    }
   }
 }
 
-unsigned blocks_for(long long threads) {
-  return (unsigned)((threads + kCacheThreads - 1) / kCacheThreads);
+// Rows per lane group: several once a launch has more rows than the device holds
+// threads for (2048 per SM) anyway.
+constexpr int kRowsPerGroup = 4;
+bool many_rows(long long rows, int lanes) { return rows * lanes > 2LL * 148 * 2048; }
+
+unsigned blocks_for(long long rows, int lanes, int u) {
+  const long long per = (long long)(kCacheThreads / lanes) * u;
+  return (unsigned)((rows + per - 1) / per);
 }
 
 }  // namespace
 
 template <int D>
 cudaError_t launch_cache_append(const CacheParams& p, cudaStream_t stream) {
+  constexpr int kLanes = D / 8, U = kRowsPerGroup;
   const long long rows = (long long)p.B * p.Hkv * p.Ln;
-  attn_cache_append_kernel<D><<<blocks_for(rows * (D / 8)), kCacheThreads, 0, stream>>>(p);
+  if (many_rows(rows, kLanes))
+    attn_cache_append_kernel<D, U><<<blocks_for(rows, kLanes, U), kCacheThreads, 0, stream>>>(p);
+  else
+    attn_cache_append_kernel<D, 1><<<blocks_for(rows, kLanes, 1), kCacheThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_cache_read(const CacheParams& p, cudaStream_t stream) {
+  constexpr int kLanes = D / 16, U = kRowsPerGroup;
   const long long rows = (long long)p.B * p.Hkv * p.Lk;
-  attn_cache_read_kernel<D><<<blocks_for(rows * (D / 16)), kCacheThreads, 0, stream>>>(p);
+  if (many_rows(rows, kLanes))
+    attn_cache_read_kernel<D, U><<<blocks_for(rows, kLanes, U), kCacheThreads, 0, stream>>>(p);
+  else
+    attn_cache_read_kernel<D, 1><<<blocks_for(rows, kLanes, 1), kCacheThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

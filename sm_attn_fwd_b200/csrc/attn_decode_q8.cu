@@ -34,9 +34,10 @@
 // sigma (a permutation of 0..7) makes both reads conflict-free in the swizzled
 // tile; P^T comes from S^T by movmatrix (8x8 transposes), with no shared memory.
 //
-// Every warp streams its own units through its own ring (TMA boxes, one mbarrier
-// per stage; lane 0 issues), so warps never wait for one another until the merge
-// at the end of the CTA: with 16-key pages eight lanes issue the boxes at once.
+// Every warp streams its own 32-key blocks through its own ring (TMA boxes, one
+// mbarrier per stage; lane 0 issues), so warps wait for one another only where a
+// piece of work (q8_sched.cuh) ends and their results are merged; with 16-key pages
+// as many lanes issue boxes as there are warps.  The ring runs on across pieces.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -49,29 +50,37 @@
 #include "cache_q8_params.h"
 #include "host_once.h"
 #include "ptx.cuh"
+#include "q8_sched.cuh"
 
 namespace attn {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;             // keys a warp takes at a time
 constexpr float kSlack = 8.0f;        // log2 units a running reference may lag behind
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// Warps per CTA (one CTA per SM): as many as the registers allow, since a warp's
+// chain of dependent steps per block, not the issue rate, is what more warps hide.
 template <int D, int NB>
 struct Q8Cfg {
-  static constexpr int kRows = 8 * NB;            // query rows per CTA
-  static constexpr int kTileBytes = kUnit * D;    // one K or V unit
+  static constexpr int kWarps = D == 128 ? (NB == 1 ? 12 : 8) : NB == 1 ? 16 : NB == 2 ? 12 : 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kRows = 8 * NB;          // query rows per unit
+  static constexpr int kTileBytes = kUnit * D;  // one K or V block
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kStages = D == 128 ? 2 : NB == 4 ? 4 : 3;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-  static constexpr int kMergeBytes = kWarps * kRows * (D + 4) * 4 + kWarps * kRows * 12;
-  static constexpr int kDataBytes = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
-  static constexpr int kOffBar = kDataBytes;
-  static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
-  static constexpr int kSmemBytes = kOffAbort + 16;
+  // merge buffers: a warp's accumulators and statistics, one 128-byte row per register
+  static constexpr int kMergeRegs = NB * (D / 16 * 4 + 6);
+  static constexpr int kMergeBytes = kWarps / 2 * kMergeRegs * 128;
+  static constexpr int kOffMerge = kRingBytes;
+  static constexpr int kOffExp = kOffMerge + kMergeBytes;  // [warp][stage][K, V][32] scale bytes
+  static constexpr int kOffBar = kOffExp + kWarps * kStages * 64;
+  static constexpr int kOffMisc = kOffBar + kWarps * kStages * 8;
+  static constexpr int kSmemBytes = kOffMisc + 64;
   static constexpr int kSmemAlloc = kSmemBytes + 1024;  // slack for 1024-byte alignment
+  static_assert(kSmemAlloc <= 227 * 1024, "shared memory");
+  static_assert(kWarps % 2 == 0 && kMergeBytes % 8 == 0, "merge buffers");
 };
 
 // Key of mma row g inside its group of 8 (see the head of this file).
@@ -119,11 +128,12 @@ __device__ __forceinline__ void ld_shared_v2(uint32_t addr, uint32_t& a, uint32_
 }  // namespace
 
 template <int D, int NB>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Q8Cfg<D, NB>::kThreads, 1)
     attn_decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const DecodeQ8Params p) {
   using C = Q8Cfg<D, NB>;
   constexpr int S = C::kStages;
+  constexpr int kWarps = C::kWarps;
   constexpr int kJ = D / 64;   // 16-byte K chunks per thread and key
   constexpr int kMu = D / 16;  // M tiles of O^T
   extern __shared__ uint8_t smem_raw[];
@@ -132,464 +142,597 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-
-  // ------------------------------------------------------------ work unit
-  // blockIdx.x = ((b * Hkv + hkv) * nsplit + split) * row_tiles + rt: the row
-  // tiles that read the same keys are neighbours and share them through L2
-  int idx = blockIdx.x;
-  const int rt = idx % p.row_tiles;
-  idx /= p.row_tiles;
-  const int split = idx % p.nsplit;
-  const int bh = idx / p.nsplit;
-  const int b = bh / p.Hkv;
-  const int hkv = bh - b * p.Hkv;
-  int kv_len = p.kv_lens[b];
-  if (kv_len < 0 || kv_len > p.Lk) {
-    if (threadIdx.x == 0 && split == 0 && rt == 0) atomicOr(p.err, kDevErrBadKvLen);
-    kv_len = kv_len < 0 ? 0 : p.Lk;
-  }
-  const int c0 = split * p.chunk;
-  const int key_end = min(c0 + p.chunk, kv_len);
-  const int rows_all = p.group * p.Lq;
-  const int rows_valid = min(C::kRows, rows_all - rt * C::kRows);
-  const long long row0 = (long long)bh * rows_all + (long long)rt * C::kRows;  // flat output row
-  const long long nrows = (long long)p.B * p.Hq * p.Lq;
-  if (c0 >= kv_len) {
-    // no key of the sequence: weight 0 for the combine, or the empty result
-    if ((int)threadIdx.x < rows_valid) {
-      if (p.nsplit > 1)
-        p.ws_lse[(long long)split * nrows + row0 + threadIdx.x] = -INFINITY;
-      else
-        p.lse[row0 + threadIdx.x] = -INFINITY;
-    }
-    if (p.nsplit == 1) {
-      uint4* dst = reinterpret_cast<uint4*>(p.o) + row0 * (D / 8);
-      for (int i = threadIdx.x; i < rows_valid * (D / 8); i += kThreads)
-        dst[i] = make_uint4(0, 0, 0, 0);
-    }
-    return;  // uniform exit
-  }
+  const int units = p.Hkv * p.row_tiles;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + warp * S;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffAbort);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc);
+  q8::Share* share = reinterpret_cast<q8::Share*>(smem + C::kOffMisc + 8);
   if (lane == 0) {
     for (int s = 0; s < S; ++s) ptx::mbar_init(&bars[s], 1);
     ptx::fence_mbar_init();
   }
-  if (threadIdx.x == 0) {
-    *abort_flag = 0;
+  if (warp == 0) {
+    const q8::Share sh =
+        q8::find_share(p.kv_lens, p.B, p.Lk, units, blockIdx.x, gridDim.x, p.err);
+    if (lane == 0) {
+      *share = sh;
+      *abort_flag = 0;
+    }
+  } else if (threadIdx.x == 32) {
     ptx::prefetch_tmap(&tm_k);
     ptx::prefetch_tmap(&tm_v);
   }
   __syncthreads();
 
   // ------------------------------------------------------------------ loads
-  const int n_units_all = (key_end - c0 + kUnit - 1) / kUnit;
-  const int n_mine = n_units_all > warp ? (n_units_all - warp + kWarps - 1) / kWarps : 0;
   uint8_t* ring = smem + warp * S * C::kStageBytes;
+  uint8_t* exps = smem + C::kOffExp + warp * S * 64;
   const bool paged = p.block_table != nullptr;
-  const int32_t* table = paged ? p.block_table + (long long)b * p.pages_per_seq : nullptr;
   const uint64_t kv_policy = ptx::l2_policy_evict_first();
-  // first key of this warp's unit i
-  auto unit_key = [&](int i) { return c0 + (warp + i * kWarps) * kUnit; };
-  // pool index (page * Hkv + hkv) of the page that holds key j, or -1 (reads as zeros)
-  auto pool = [&](int j) -> int {
-    const int pi = j >> p.page_shift;
-    if (pi >= p.pages_per_seq) return -1;
-    const int page = __ldg(table + pi);
-    if (page < 0 || page >= p.num_pages) {
-      atomicOr(p.err, kDevErrBadPage);
-      return -1;
+  // The block this warp loads next: keys [l_key, l_end) of piece `lw` hold it and the
+  // warp's later ones; z: pool index (page * Hkv + hkv) of the page of this lane's key,
+  // -1 past the end or for a page id outside the pool (reads as zeros).
+  q8::Walk lw;
+  lw.start(*share, p.kv_lens, p.Lk);
+  int l_key = 0, l_end = 0, z = -1;
+  auto find_block = [&]() {  // move to a piece with a block for this warp, and fetch its page
+    while (lw.valid() && l_key >= l_end) {
+      lw.next(p.kv_lens, p.Lk, units);
+      l_key = lw.t0 * 128 + warp * kUnit;
+      l_end = min(lw.t1 * 128, lw.len);
     }
-    return page * p.Hkv + hkv;
+    if (!lw.valid()) return;
+    const int hkv = lw.h / p.row_tiles;
+    z = lw.b * p.Hkv + hkv;
+    if (paged) {
+      z = -1;
+      const int j = l_key + lane;
+      if (j < l_end) {
+        const int page = __ldg(p.block_table + (long long)lw.b * p.pages_per_seq +
+                               (j >> p.page_shift));
+        if (page >= 0 && page < p.num_pages)
+          z = page * p.Hkv + hkv;
+        else
+          atomicOr(p.err, kDevErrBadPage);
+      }
+    }
   };
-  // Lane 0 issues unit i's boxes: one per operand, or one per page slice for
-  // pages shorter than a unit.
-  auto issue = [&](int i) {
-    const int s = i % S;
-    const uint32_t bar = ptx::smem_u32(&bars[s]);
+  l_key = lw.t0 * 128 + warp * kUnit;
+  l_end = min(lw.t1 * 128, lw.len);
+  find_block();
+  int n_issued = 0;
+  int pend_ke = 1, pend_ve = 1;  // scale bytes of the block issued last, not stored yet
+  auto store_exps = [&]() {
+    if (n_issued == 0) return;
+    uint8_t* dst = exps + (n_issued - 1) % S * 64;
+    dst[lane] = (uint8_t)pend_ke;
+    dst[32 + lane] = (uint8_t)pend_ve;
+  };
+  // Issue the boxes of the next block (one per operand, or one per page slice for pages
+  // shorter than a block), load its scale bytes and find the block after it.
+  auto issue = [&]() {
+    const int s = n_issued % S;
     uint8_t* kd = ring + s * C::kStageBytes;
     uint8_t* vd = kd + C::kTileBytes;
-    const int k0 = unit_key(i);
-    ptx::mbar_arrive_expect_tx_a(bar, C::kStageBytes);
-    if (!paged) {
-      ptx::tma_load_3d_hint(kd, &tm_k, &bars[s], 0, k0, bh, kv_policy);
-      ptx::tma_load_3d_hint(vd, &tm_v, &bars[s], 0, k0, bh, kv_policy);
-    } else if (p.page_size >= kUnit) {
-      const int z = pool(k0), y = k0 & (p.page_size - 1);
-      ptx::tma_load_3d_hint(kd, &tm_k, &bars[s], 0, y, z, kv_policy);
-      ptx::tma_load_3d_hint(vd, &tm_v, &bars[s], 0, y, z, kv_policy);
-    } else {
-      for (int r = 0; r < kUnit; r += p.page_size) {
-        const int z = k0 + r < key_end ? pool(k0 + r) : -1;  // ids past the last page: never read
-        ptx::tma_load_3d_hint(kd + r * D, &tm_k, &bars[s], 0, 0, z, kv_policy);
-        ptx::tma_load_3d_hint(vd + r * D, &tm_v, &bars[s], 0, 0, z, kv_policy);
-      }
+    if (lane == 0) ptx::mbar_arrive_expect_tx(&bars[s], C::kStageBytes);
+    __syncwarp();
+    const int rows = paged ? min(p.page_size, kUnit) : kUnit;
+    if ((lane & (rows - 1)) == 0) {
+      const int j = l_key + lane;
+      const int y = paged ? j & (p.page_size - 1) : j;
+      ptx::tma_load_3d_hint(kd + lane * D, &tm_k, &bars[s], 0, y, z, kv_policy);
+      ptx::tma_load_3d_hint(vd + lane * D, &tm_v, &bars[s], 0, y, z, kv_policy);
     }
-  };
-  // Lane l's scale bytes of unit i's key l (keys past the end: any valid byte)
-  auto load_exps = [&](int i, int& ke, int& ve) {
-    ke = ve = 127;
-    const int j = unit_key(i) + lane;
-    if (i >= n_mine || j >= key_end) return;
-    long long at;
-    if (!paged) {
-      at = (long long)bh * p.Lk + j;
-    } else {
-      const int z = pool(j);
-      if (z < 0) return;
-      at = ((long long)z << p.page_shift) + (j & (p.page_size - 1));
+    pend_ke = pend_ve = 1;
+    const int j = l_key + lane;
+    if (j < l_end && z >= 0) {
+      const long long at = paged ? ((long long)z << p.page_shift) + (j & (p.page_size - 1))
+                                 : (long long)z * p.Lk + j;
+      pend_ke = __ldg(p.k_exp + at);
+      pend_ve = __ldg(p.v_exp + at);
     }
-    ke = __ldg(p.k_exp + at);
-    ve = __ldg(p.v_exp + at);
+    ++n_issued;
+    l_key += kWarps * kUnit;
+    find_block();
   };
-  int n_issued = min(n_mine, S);
-  if (lane == 0)
-    for (int i = 0; i < n_issued; ++i) issue(i);
-  int ke_next, ve_next;
-  load_exps(0, ke_next, ve_next);
-
-  // ------------------------------------------------------------------- Q
-  // B operand of S^T: query row n = g of each 8-row block, d in the order above
-  uint32_t qf[NB][kJ * 4][2];
-  float fac0[NB], fac1[NB];  // scale * log2 e * 2^(row shift) of query rows 2t and 2t + 1
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    uint4 raw[kJ][2];
-    const int r = nb * 8 + g;
-#pragma unroll
-    for (int j = 0; j < kJ; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        raw[j][h] = r < rows_valid
-                        ? __ldg(reinterpret_cast<const uint4*>(p.q) + (row0 + r) * (D / 8) +
-                                j * 8 + t * 2 + h)
-                        : make_uint4(0, 0, 0, 0);
-    float amax = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kJ; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t w[4] = {raw[j][h].x, raw[j][h].y, raw[j][h].z, raw[j][h].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[i] << 16)),
-                                   fabsf(__uint_as_float(w[i] & 0xffff0000u))));
-      }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // the row times 2^(14 - exponent of amax), so that its largest lies in [2^14, 2^15);
-    // in two factors, as 2^(14 + 126) is no fp32 number
-    const int ex = max((int)(__float_as_uint(amax) >> 23), 1) - 127;
-    const int sh = 14 - ex;
-    const float s1 = __uint_as_float((uint32_t)(127 + sh / 2) << 23);
-    const float s2 = __uint_as_float((uint32_t)(127 + sh - sh / 2) << 23);
-#pragma unroll
-    for (int j = 0; j < kJ; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t w[4] = {raw[j][h].x, raw[j][h].y, raw[j][h].z, raw[j][h].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          qf[nb][j * 4 + h * 2 + (i >> 1)][i & 1] =
-              pack_f16x2(__uint_as_float(w[i] << 16) * s1 * s2,
-                         __uint_as_float(w[i] & 0xffff0000u) * s1 * s2);
-      }
-    // rows 2t and 2t + 1 live in lanes 8t and 8t + 4
-    const int sh0 = __shfl_sync(0xffffffffu, sh, 8 * t);
-    const int sh1 = __shfl_sync(0xffffffffu, sh, 8 * t + 4);
-    fac0[nb] = p.scale_log2 * __uint_as_float((uint32_t)(127 - sh0 / 2) << 23) *
-               __uint_as_float((uint32_t)(127 - (sh0 - sh0 / 2)) << 23);
-    fac1[nb] = p.scale_log2 * __uint_as_float((uint32_t)(127 - sh1 / 2) << 23) *
-               __uint_as_float((uint32_t)(127 - (sh1 - sh1 / 2)) << 23);
+  for (int i = 0; i < S && lw.valid(); ++i) {
+    store_exps();
+    issue();
   }
 
-  // --------------------------------------------------------------- main loop
-  float o[NB][kMu][4];
-  float m[NB][2], R[NB][2], l[NB][2];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-    for (int mu = 0; mu < kMu; ++mu)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[nb][mu][i] = 0.0f;
-    m[nb][0] = m[nb][1] = R[nb][0] = R[nb][1] = -INFINITY;
-    l[nb][0] = l[nb][1] = 0.0f;
-  }
   const int sg = sigma<D>(g), s2t0 = sigma<D>(2 * t), s2t1 = sigma<D>(2 * t + 1);
   bool ok = true;
-  int done = 0;
-  for (; done < n_mine; ++done) {
-    const int s = done % S;
-    const int k0 = unit_key(done);
-    const int left = key_end - k0;  // visible keys of the unit: [0, left)
-    const int ke = ke_next, ve = ve_next;
-    load_exps(done + 1, ke_next, ve_next);
-    ok = ptx::mbar_wait_a(ptx::smem_u32(&bars[s]), (uint32_t)(done / S) & 1u, abort_flag, p.err,
-                          kDevErrTimeoutProducer);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    const uint32_t sk = ptx::smem_u32(ring + s * C::kStageBytes);
-    const uint32_t sv = sk + C::kTileBytes;
+  int done = 0;  // blocks consumed
+  float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
+  q8::Walk w;
+  for (w.start(*share, p.kv_lens, p.Lk); w.valid(); w.next(p.kv_lens, p.Lk, units)) {
+    const int hkv = w.h / p.row_tiles, rt = w.h - hkv * p.row_tiles;
+    const int rows_all = p.group * p.Lq;
+    const int rows_valid = min(C::kRows, rows_all - rt * C::kRows);
+    // flat output row of the unit's first row
+    const long long row0 =
+        ((long long)w.b * p.Hkv + hkv) * rows_all + (long long)rt * C::kRows;
+    const int key_end = min(w.t1 * 128, w.len);
 
-    // S^T of both 16-key blocks
-    float z[2][NB][4];
+    // ----------------------------------------------------------------- Q
+    // B operand of S^T: query row n = g of each 8-row block, d in the order above
+    uint32_t qf[NB][kJ * 4][2];
+    float fac0[NB], fac1[NB];  // scale * log2 e * 2^(row shift) of query rows 2t and 2t + 1
 #pragma unroll
-    for (int blk = 0; blk < 2; ++blk) {
+    for (int nb = 0; nb < NB; ++nb) {
+      uint4 raw[kJ][2];
+      const int r = nb * 8 + g;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int j = 0; j < kJ; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z[blk][nb][i] = 0.0f;
+        for (int h = 0; h < 2; ++h)
+          raw[j][h] = r < rows_valid
+                          ? __ldg(reinterpret_cast<const uint4*>(p.q) + (row0 + r) * (D / 8) +
+                                  j * 8 + t * 2 + h)
+                          : make_uint4(0, 0, 0, 0);
+      float amax = 0.0f;
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        uint32_t wa[4], wb[4];
-        ptx::ld_shared_v4(sk + chunk_off<D>(blk * 16 + sg, j * 4 + t), wa[0], wa[1], wa[2], wa[3]);
-        ptx::ld_shared_v4(sk + chunk_off<D>(blk * 16 + 8 + sg, j * 4 + t), wb[0], wb[1], wb[2],
-                          wb[3]);
+      for (int j = 0; j < kJ; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t a0, a1, a2, a3;
-          q8::codes4_to_f16(wa[i], a0, a2);
-          q8::codes4_to_f16(wb[i], a1, a3);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t x[4] = {raw[j][h].x, raw[j][h].y, raw[j][h].z, raw[j][h].w};
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-            mma16816(z[blk][nb], a0, a1, a2, a3, qf[nb][j * 4 + i][0], qf[nb][j * 4 + i][1]);
+          for (int i = 0; i < 4; ++i)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[i] << 16)),
+                                     fabsf(__uint_as_float(x[i] & 0xffff0000u))));
         }
-      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // the row times 2^(14 - exponent of amax), so that its largest lies in [2^14, 2^15);
+      // in two factors, as 2^(14 + 126) is no fp32 number
+      const int ex = max((int)(__float_as_uint(amax) >> 23), 1) - 127;
+      const int sh = 14 - ex;
+      const float s1 = __uint_as_float((uint32_t)(127 + sh / 2) << 23);
+      const float s2 = __uint_as_float((uint32_t)(127 + sh - sh / 2) << 23);
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t x[4] = {raw[j][h].x, raw[j][h].y, raw[j][h].z, raw[j][h].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            qf[nb][j * 4 + h * 2 + (i >> 1)][i & 1] =
+                pack_f16x2(__uint_as_float(x[i] << 16) * s1 * s2,
+                           __uint_as_float(x[i] & 0xffff0000u) * s1 * s2);
+        }
+      // rows 2t and 2t + 1 live in lanes 8t and 8t + 4
+      const int sh0 = __shfl_sync(0xffffffffu, sh, 8 * t);
+      const int sh1 = __shfl_sync(0xffffffffu, sh, 8 * t + 4);
+      fac0[nb] = p.scale_log2 * __uint_as_float((uint32_t)(127 - sh0 / 2) << 23) *
+                 __uint_as_float((uint32_t)(127 - (sh0 - sh0 / 2)) << 23);
+      fac1[nb] = p.scale_log2 * __uint_as_float((uint32_t)(127 - sh1 / 2) << 23) *
+                 __uint_as_float((uint32_t)(127 - (sh1 - sh1 / 2)) << 23);
     }
-    // scores in the base-2 domain; z[..][i]: key blk * 16 + (i / 2) * 8 + sigma(g), row 2t + i % 2
-    float vexp[2][2];
+
+    // ------------------------------------------------------------- key blocks
+    float o[NB][kMu][4];
+    float m[NB][2], R[NB][2], l[NB][2];
 #pragma unroll
-    for (int blk = 0; blk < 2; ++blk)
+    for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int key = blk * 16 + h * 8 + sg;
-        const float ks = q8::scale_of(__shfl_sync(0xffffffffu, ke, key));
-        vexp[blk][h] = (float)(__shfl_sync(0xffffffffu, ve, key) - 127);
-        const bool vis = key < left;
+      for (int mu = 0; mu < kMu; ++mu)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          z[blk][nb][2 * h] = vis ? z[blk][nb][2 * h] * (ks * fac0[nb]) : -INFINITY;
-          z[blk][nb][2 * h + 1] = vis ? z[blk][nb][2 * h + 1] * (ks * fac1[nb]) : -INFINITY;
-        }
-      }
-    // running references: raised only when a score passes one by more than kSlack
-    bool need = false;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float zm = fmaxf(fmaxf(z[0][nb][i], z[0][nb][2 + i]),
-                               fmaxf(z[1][nb][i], z[1][nb][2 + i]));
-        const float wm = fmaxf(fmaxf(z[0][nb][i] + vexp[0][0], z[0][nb][2 + i] + vexp[0][1]),
-                               fmaxf(z[1][nb][i] + vexp[1][0], z[1][nb][2 + i] + vexp[1][1]));
-        need |= zm > m[nb][i] + kSlack || wm > R[nb][i] + kSlack;
-      }
-    if (__any_sync(0xffffffffu, need)) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float zm = fmaxf(fmaxf(z[0][nb][i], z[0][nb][2 + i]),
-                           fmaxf(z[1][nb][i], z[1][nb][2 + i]));
-          float wm = fmaxf(fmaxf(z[0][nb][i] + vexp[0][0], z[0][nb][2 + i] + vexp[0][1]),
-                           fmaxf(z[1][nb][i] + vexp[1][0], z[1][nb][2 + i] + vexp[1][1]));
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) {
-            zm = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, x));
-            wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, x));
-          }
-          if (zm > m[nb][i]) {
-            l[nb][i] *= ptx::ex2(m[nb][i] - zm);
-            m[nb][i] = zm;
-          }
-          if (wm > R[nb][i]) {
-            const float a = ptx::ex2(R[nb][i] - wm);
-            R[nb][i] = wm;
-#pragma unroll
-            for (int mu = 0; mu < kMu; ++mu) {
-              o[nb][mu][i] *= a;
-              o[nb][mu][2 + i] *= a;
-            }
-          }
-        }
+        for (int i = 0; i < 4; ++i) o[nb][mu][i] = 0.0f;
+      m[nb][0] = m[nb][1] = R[nb][0] = R[nb][1] = -INFINITY;
+      l[nb][0] = l[nb][1] = 0.0f;
     }
-    // row sums and P^T (times the value scales) as the B operand of O^T
-    uint32_t pb[2][NB][2];
+    for (int k0 = w.t0 * 128 + warp * kUnit; k0 < key_end && ok; k0 += kWarps * kUnit) {
+      const int s = done % S;
+      const int left = key_end - k0;  // visible keys of the block: [0, left)
+      ok = ptx::mbar_wait_a(ptx::smem_u32(&bars[s]), (uint32_t)(done / S) & 1u, abort_flag, p.err,
+                            kDevErrTimeoutProducer);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      // the bytes of the block issued last: this block's, if the ring has just started
+      store_exps();
+      __syncwarp();
+      const uint32_t sk = ptx::smem_u32(ring + s * C::kStageBytes);
+      const uint32_t sv = sk + C::kTileBytes;
+      const uint8_t* eb = exps + s * 64;
+
+      // S^T of both 16-key blocks
+      float z[2][NB][4];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+      for (int blk = 0; blk < 2; ++blk) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[blk][nb][i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          uint32_t wa[4], wb[4];
+          ptx::ld_shared_v4(sk + chunk_off<D>(blk * 16 + sg, j * 4 + t), wa[0], wa[1], wa[2], wa[3]);
+          ptx::ld_shared_v4(sk + chunk_off<D>(blk * 16 + 8 + sg, j * 4 + t), wb[0], wb[1], wb[2],
+                            wb[3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t a0, a1, a2, a3;
+            q8::codes4_to_f16(wa[i], a0, a2);
+            q8::codes4_to_f16(wb[i], a1, a3);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              mma16816(z[blk][nb], a0, a1, a2, a3, qf[nb][j * 4 + i][0], qf[nb][j * 4 + i][1]);
+          }
+        }
+      }
+      // scores in the base-2 domain; z[..][i]: key blk * 16 + (i / 2) * 8 + sigma(g), row 2t + i % 2
+      float vexp[2][2];
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float z0 = z[blk][nb][2 * h], z1 = z[blk][nb][2 * h + 1];
-          l[nb][0] += ptx::ex2(z0 - m[nb][0]);
-          l[nb][1] += ptx::ex2(z1 - m[nb][1]);
-          const float w0 = ptx::ex2(z0 + vexp[blk][h] - R[nb][0]);
-          const float w1 = ptx::ex2(z1 + vexp[blk][h] - R[nb][1]);
-          pb[blk][nb][h] = transpose8x8(pack_f16x2(w0, w1));
+          const int key = blk * 16 + h * 8 + sg;
+          const float ks = q8::scale_of(eb[key]);
+          vexp[blk][h] = (float)((int)eb[32 + key] - 127);
+          const bool vis = key < left;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            z[blk][nb][2 * h] = vis ? z[blk][nb][2 * h] * (ks * fac0[nb]) : -INFINITY;
+            z[blk][nb][2 * h + 1] = vis ? z[blk][nb][2 * h + 1] * (ks * fac1[nb]) : -INFINITY;
+          }
         }
-    // O^T += V^T P^T
+      // running references: raised only when a score passes one by more than kSlack
+      bool need = false;
 #pragma unroll
-    for (int blk = 0; blk < 2; ++blk) {
-      const int ka = blk * 16 + s2t0, kb = blk * 16 + s2t1;
-      constexpr int kW = D / 32;  // words per thread and key
-      uint32_t w[4][kW];
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = (i & 1 ? kb : ka) + (i >> 1) * 8;
-        if constexpr (D == 128)
-          ptx::ld_shared_v4(sv + chunk_off<D>(key, g), w[i][0], w[i][1], w[i][2], w[i][3]);
-        else
-          ld_shared_v2(sv + chunk_off<D>(key, g >> 1) + (g & 1) * 8, w[i][0], w[i][1]);
-        // a masked key's codes may be anything (even NaN): 0 * NaN would poison O
-        if (left < kUnit && key >= left) {
+        for (int i = 0; i < 2; ++i) {
+          const float zm = fmaxf(fmaxf(z[0][nb][i], z[0][nb][2 + i]),
+                                 fmaxf(z[1][nb][i], z[1][nb][2 + i]));
+          const float wm = fmaxf(fmaxf(z[0][nb][i] + vexp[0][0], z[0][nb][2 + i] + vexp[0][1]),
+                                 fmaxf(z[1][nb][i] + vexp[1][0], z[1][nb][2 + i] + vexp[1][1]));
+          need |= zm > m[nb][i] + kSlack || wm > R[nb][i] + kSlack;
+        }
+      if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
-          for (int x = 0; x < kW; ++x) w[i][x] = 0u;
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float zm = fmaxf(fmaxf(z[0][nb][i], z[0][nb][2 + i]),
+                             fmaxf(z[1][nb][i], z[1][nb][2 + i]));
+            float wm = fmaxf(fmaxf(z[0][nb][i] + vexp[0][0], z[0][nb][2 + i] + vexp[0][1]),
+                             fmaxf(z[1][nb][i] + vexp[1][0], z[1][nb][2 + i] + vexp[1][1]));
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) {
+              zm = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, x));
+              wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, x));
+            }
+            if (zm > m[nb][i]) {
+              l[nb][i] *= ptx::ex2(m[nb][i] - zm);
+              m[nb][i] = zm;
+            }
+            if (wm > R[nb][i]) {
+              const float a = ptx::ex2(R[nb][i] - wm);
+              R[nb][i] = wm;
+#pragma unroll
+              for (int mu = 0; mu < kMu; ++mu) {
+                o[nb][mu][i] *= a;
+                o[nb][mu][2 + i] *= a;
+              }
+            }
+          }
+      }
+      // row sums and P^T (times the value scales) as the B operand of O^T
+      uint32_t pb[2][NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float z0 = z[blk][nb][2 * h], z1 = z[blk][nb][2 * h + 1];
+            l[nb][0] += ptx::ex2(z0 - m[nb][0]);
+            l[nb][1] += ptx::ex2(z1 - m[nb][1]);
+            const float w0 = ptx::ex2(z0 + vexp[blk][h] - R[nb][0]);
+            const float w1 = ptx::ex2(z1 + vexp[blk][h] - R[nb][1]);
+            pb[blk][nb][h] = transpose8x8(pack_f16x2(w0, w1));
+          }
+      // O^T += V^T P^T
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk) {
+        const int ka = blk * 16 + s2t0, kb = blk * 16 + s2t1;
+        constexpr int kW = D / 32;  // words per thread and key
+        uint32_t vw[4][kW];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = (i & 1 ? kb : ka) + (i >> 1) * 8;
+          if constexpr (D == 128)
+            ptx::ld_shared_v4(sv + chunk_off<D>(key, g), vw[i][0], vw[i][1], vw[i][2], vw[i][3]);
+          else
+            ld_shared_v2(sv + chunk_off<D>(key, g >> 1) + (g & 1) * 8, vw[i][0], vw[i][1]);
+          // a masked key's codes may be anything (even NaN): 0 * NaN would poison O
+          if (left < kUnit && key >= left) {
+#pragma unroll
+            for (int x = 0; x < kW; ++x) vw[i][x] = 0u;
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < kW; ++x)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t sel = h ? 0x7362 : 0x5140;  // bytes 2h, 2h + 1 of both keys, interleaved
+            uint32_t a0, a1, a2, a3;
+            q8::codes4_to_f16(__byte_perm(vw[0][x], vw[1][x], sel), a0, a1);
+            q8::codes4_to_f16(__byte_perm(vw[2][x], vw[3][x], sel), a2, a3);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              mma16816(o[nb][2 * x + h], a0, a1, a2, a3, pb[blk][nb][0], pb[blk][nb][1]);
+          }
+      }
+      // every lane has read the stage: the next block may land there
+      __syncwarp();
+      ++done;
+      if (lw.valid()) issue();
+    }
+
+    // ----------------------------------------------------------------- merge
+    // Pairwise: the upper half of the warps leaves O (in units of 2^R), m, R and its
+    // lanes' parts of l in shared memory, the lower half adds them to its own; lane by
+    // lane, as every warp has the same layout.
+    ok = __syncthreads_and(ok ? 1 : 0) != 0;  // also: the buffers are free again
+    for (int n = kWarps; n > 1;) {
+      const int half = (n + 1) / 2;
+      if (warp >= half && warp < n) {
+        float* dst = merge + (warp - half) * (C::kMergeRegs * 32) + lane;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            dst[(nb * 6 + i) * 32] = m[nb][i];
+            dst[(nb * 6 + 2 + i) * 32] = R[nb][i];
+            dst[(nb * 6 + 4 + i) * 32] = l[nb][i];
+          }
+#pragma unroll
+          for (int mu = 0; mu < kMu; ++mu)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[(NB * 6 + (nb * kMu + mu) * 4 + i) * 32] = o[nb][mu][i];
         }
       }
+      __syncthreads();
+      if (warp < n - half) {
+        const float* src = merge + warp * (C::kMergeRegs * 32) + lane;
 #pragma unroll
-      for (int x = 0; x < kW; ++x)
+        for (int nb = 0; nb < NB; ++nb) {
+          float a0[2], a1[2];  // weights of this warp's and the other's O
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t sel = h ? 0x7362 : 0x5140;  // bytes 2h, 2h + 1 of both keys, interleaved
-          uint32_t a0, a1, a2, a3;
-          q8::codes4_to_f16(__byte_perm(w[0][x], w[1][x], sel), a0, a1);
-          q8::codes4_to_f16(__byte_perm(w[2][x], w[3][x], sel), a2, a3);
+          for (int i = 0; i < 2; ++i) {
+            const float m1 = src[(nb * 6 + i) * 32], R1 = src[(nb * 6 + 2 + i) * 32];
+            const float mn = fmaxf(m[nb][i], m1), Rn = fmaxf(R[nb][i], R1);
+            const float mu0 = mn == -INFINITY ? 0.0f : mn, Ru0 = Rn == -INFINITY ? 0.0f : Rn;
+            l[nb][i] = l[nb][i] * ptx::ex2(m[nb][i] - mu0) +
+                       src[(nb * 6 + 4 + i) * 32] * ptx::ex2(m1 - mu0);
+            a0[i] = ptx::ex2(R[nb][i] - Ru0);
+            a1[i] = ptx::ex2(R1 - Ru0);
+            m[nb][i] = mn;
+            R[nb][i] = Rn;
+          }
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-            mma16816(o[nb][2 * x + h], a0, a1, a2, a3, pb[blk][nb][0], pb[blk][nb][1]);
+          for (int mu = 0; mu < kMu; ++mu)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              o[nb][mu][i] = o[nb][mu][i] * a0[i & 1] +
+                             src[(NB * 6 + (nb * kMu + mu) * 4 + i) * 32] * a1[i & 1];
+        }
+      }
+      n = half;
+      if (n > 1) __syncthreads();
+    }
+    if (warp == 0) {
+      // thread (g, t): d = (D / 8) g .. + D / 8 - 1 of query rows 2t and 2t + 1
+      const bool final = w.whole();
+      const long long at = final ? 0 : (long long)w.slot(blockIdx.x) * C::kRows;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float ls = l[nb][i];
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
+          const int r = nb * 8 + 2 * t + i;
+          const bool have = ok && ls > 0.0f;
+          const float mu0 = m[nb][i] == -INFINITY ? 0.0f : m[nb][i];
+          const float lse = have ? (mu0 + ptx::lg2(ls)) * kLn2 : -INFINITY;
+          // O is in units of 2^R, l in units of 2^m
+          const float inv = have ? 1.0f / ls : 0.0f;
+          const float f = R[nb][i] == -INFINITY ? 0.0f : ptx::ex2(R[nb][i] - mu0);
+          float v[2 * kMu];
+#pragma unroll
+          for (int mu = 0; mu < kMu; ++mu) {
+            v[2 * mu] = o[nb][mu][i] * inv * f;
+            v[2 * mu + 1] = o[nb][mu][2 + i] * inv * f;
+          }
+          if (r >= rows_valid) continue;
+          if (final) {
+            uint4* dst = reinterpret_cast<uint4*>(p.o) + (row0 + r) * (D / 8) + g * (D / 64);
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x)
+              dst[x] = make_uint4(ptx::pack_bf16x2(v[8 * x], v[8 * x + 1]),
+                                  ptx::pack_bf16x2(v[8 * x + 2], v[8 * x + 3]),
+                                  ptx::pack_bf16x2(v[8 * x + 4], v[8 * x + 5]),
+                                  ptx::pack_bf16x2(v[8 * x + 6], v[8 * x + 7]));
+            if (g == 0) p.lse[row0 + r] = lse;
+          } else {
+            float4* dst = reinterpret_cast<float4*>(p.ws_o + (at + r) * D + g * (D / 8));
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x)
+              dst[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+            if (g == 0) p.ws_lse[at + r] = lse;
+          }
         }
     }
-    // every lane has read the stage: the next unit may land there
-    __syncwarp();
-    if (done + S < n_mine) {
-      if (lane == 0) issue(done + S);
-      ++n_issued;
-    }
+    if (!ok) break;
   }
   if (!ok && lane == 0) {
-    // a wait gave up: let the copies in flight land before the CTA goes on
+    // a wait gave up: let the copies in flight land before the CTA goes away
     for (int i = done; i < n_issued; ++i) {
       int dummy = 0;
       ptx::mbar_wait_a(ptx::smem_u32(&bars[i % S]), (uint32_t)(i / S) & 1u, &dummy, nullptr, 0);
     }
   }
+}
 
-  // ------------------------------------------------------------------ merge
-  // Each warp leaves O (in units of 2^R), m, R and l of its rows in shared
-  // memory (the ring's); rows are padded by 4 floats against bank conflicts.
-  constexpr int kLd = D + 4;
-  float* mo = reinterpret_cast<float*>(smem);
-  float* stat = mo + kWarps * C::kRows * kLd;  // [3][warp][row]
-  __syncthreads();
+// Returns once the kernel before this one in the stream is complete and its writes
+// are visible (this one may have started earlier).
+__device__ __forceinline__ void wait_for_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Merges the pieces of units that several CTAs computed,
+//   LSE = log sum_s exp(LSE_s),  O = sum_s exp(LSE_s - LSE) O_s,
+// and writes the empty result of sequences without keys.  One warp per output row;
+// lane i owns d / 32 consecutive elements.
+template <int D>
+__global__ void __launch_bounds__(256) attn_decode_q8_combine_kernel(const DecodeQ8Params p) {
+  constexpr int kPer = D / 32;
+  constexpr float kLog2e = 1.44269504088896340736f;
+  const long long nrows = (long long)p.B * p.Hq * p.Lq;
+  const long long row = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= nrows) {  // warp-uniform
+    wait_for_previous_kernel();
+    return;
+  }
+  const int rows_all = p.group * p.Lq;
+  const int bh = (int)(row / rows_all);
+  const int r = (int)(row - (long long)bh * rows_all);
+  const int b = bh / p.Hkv;
+  const int units = p.Hkv * p.row_tiles;
+  const int unit = (bh - b * p.Hkv) * p.row_tiles + r / p.tile_rows;
+  const int rr = r % p.tile_rows;
+  // the line's tiles, and those before sequence b
+  long long all = 0, before = 0;
+  for (int i = lane; i < p.B; i += 32) {
+    const int n = q8::tiles_of(q8::seq_len(p.kv_lens, i, p.Lk));
+    all += n;
+    if (i < b) before += n;
+  }
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  const int tiles = q8::tiles_of(q8::seq_len(p.kv_lens, b, p.Lk));
+  // every thread waits, so that whatever follows this kernel follows the one before it
+  wait_for_previous_kernel();
+  __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + row * D + lane * kPer;
+  float acc[kPer];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float ls = l[nb][i];
+  for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
+  float lse = -INFINITY;
+  if (tiles > 0) {
+    const long long T = all * units;
+    const long long base = before * units + (long long)unit * tiles;
+    const int G = q8::ctas_used(T, p.num_ctas);
+    const long long c0 = q8::cta_of(base, T, G), c1 = q8::cta_of(base + tiles - 1, T, G);
+    if (c0 == c1) return;  // written by its CTA
+    const int n = (int)(c1 - c0) + 1;
+    // piece i of the unit: the start (slot 2 c0 + 1), then the ends and middles (2 c)
+    auto slot_row = [&](int i) {
+      return (2 * (c0 + i) + (i == 0 ? 1 : 0)) * p.tile_rows + rr;
+    };
+    float mx = -INFINITY;
+    for (int i = lane; i < n; i += 32) mx = fmaxf(mx, p.ws_lse[slot_row(i)]);
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
-      const int r = nb * 8 + 2 * t + i;
-      if (g == 0) {
-        stat[warp * C::kRows + r] = m[nb][i];
-        stat[(kWarps + warp) * C::kRows + r] = R[nb][i];
-        stat[(2 * kWarps + warp) * C::kRows + r] = ls;
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    float sum = 0.0f;
+    if (mx != -INFINITY) {
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const float ls = i0 + lane < n ? p.ws_lse[slot_row(i0 + lane)] : -INFINITY;
+        const float wl = ls == -INFINITY ? 0.0f : ptx::ex2((ls - mx) * kLog2e);
+        sum += wl;
+        const int k = min(32, n - i0);
+#pragma unroll 4
+        for (int i = 0; i < k; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, wl, i);
+          const float* src = p.ws_o + slot_row(i0 + i) * D + lane * kPer;
+          if constexpr (kPer == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            acc[0] += wi * v.x;
+            acc[1] += wi * v.y;
+            acc[2] += wi * v.z;
+            acc[3] += wi * v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            acc[0] += wi * v.x;
+            acc[1] += wi * v.y;
+          }
+        }
       }
-      // d of o[nb][mu][i] and o[nb][mu][2 + i]: (D / 8) g + 2 mu, + 1
-      float* dst = mo + (warp * C::kRows + r) * kLd + g * (D / 8);
 #pragma unroll
-      for (int mu = 0; mu < kMu; mu += 2)
-        *reinterpret_cast<float4*>(dst + 2 * mu) =
-            make_float4(o[nb][mu][i], o[nb][mu][2 + i], o[nb][mu + 1][i], o[nb][mu + 1][2 + i]);
-    }
-  __syncthreads();
-  for (int i = threadIdx.x; i < rows_valid * (D / 4); i += kThreads) {
-    const int r = i / (D / 4), c = i - r * (D / 4);
-    float M = -INFINITY, Rm = -INFINITY;
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const float inv = 1.0f / sum;  // the piece of LSE mx has weight 1
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      M = fmaxf(M, stat[w * C::kRows + r]);
-      Rm = fmaxf(Rm, stat[(kWarps + w) * C::kRows + r]);
-    }
-    const float Mu = M == -INFINITY ? 0.0f : M, Ru = Rm == -INFINITY ? 0.0f : Rm;
-    float L = 0.0f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      L += stat[(2 * kWarps + w) * C::kRows + r] * ptx::ex2(stat[w * C::kRows + r] - Mu);
-      const float a = ptx::ex2(stat[(kWarps + w) * C::kRows + r] - Ru);
-      const float4 v = *reinterpret_cast<const float4*>(mo + (w * C::kRows + r) * kLd + c * 4);
-      acc.x += a * v.x;
-      acc.y += a * v.y;
-      acc.z += a * v.z;
-      acc.w += a * v.w;
-    }
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    const float f = ptx::ex2(Ru - Mu);  // O is in units of 2^R, L in units of 2^m
-    acc.x = acc.x * inv * f;
-    acc.y = acc.y * inv * f;
-    acc.z = acc.z * inv * f;
-    acc.w = acc.w * inv * f;
-    const long long row = row0 + r;
-    if (p.nsplit > 1) {
-      *reinterpret_cast<float4*>(p.ws_o + ((long long)split * nrows + row) * D + c * 4) = acc;
-    } else {
-      uint2 v;
-      v.x = ptx::pack_bf16x2(acc.x, acc.y);
-      v.y = ptx::pack_bf16x2(acc.z, acc.w);
-      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.o) + row * D + c * 4) = v;
-    }
-    if (c == 0) {
-      const float lse = L > 0.0f ? (Mu + ptx::lg2(L)) * kLn2 : -INFINITY;
-      if (p.nsplit > 1)
-        p.ws_lse[(long long)split * nrows + row] = lse;
-      else
-        p.lse[row] = lse;
+      for (int i = 0; i < kPer; ++i) acc[i] *= inv;
+      lse = mx + ptx::lg2(sum) * kLn2;
     }
   }
+  if constexpr (kPer == 4)
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(ptx::pack_bf16x2(acc[0], acc[1]), ptx::pack_bf16x2(acc[2], acc[3]));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = ptx::pack_bf16x2(acc[0], acc[1]);
+  if (lane == 0) p.lse[row] = lse;
 }
 
 namespace {
 
 template <int D, int NB>
-cudaError_t launch_nb(const CUtensorMap& tk, const CUtensorMap& tv, DecodeQ8Params p,
+cudaError_t launch_nb(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeQ8Params& p,
                       cudaStream_t stream) {
+  using C = Q8Cfg<D, NB>;
   auto kern = attn_decode_q8_kernel<D, NB>;
-  constexpr int smem = Q8Cfg<D, NB>::kSmemAlloc;
   static PerContextOnce once;
   const cudaError_t e = once_per_context(once, [&](int) {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemAlloc);
   });
   if (e != cudaSuccess) return e;
-  const int rows = p.group * p.Lq;
-  p.row_tiles = (rows + 8 * NB - 1) / (8 * NB);
-  const long long grid = (long long)p.B * p.Hkv * p.nsplit * p.row_tiles;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  kern<<<(unsigned)grid, kThreads, smem, stream>>>(tk, tv, p);
+  kern<<<p.num_ctas, C::kThreads, C::kSmemAlloc, stream>>>(tk, tv, p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-// Query rows per CTA: 8, 16 or 32, the smallest that holds the group's rows (32
-// is the most whose accumulators fit in the registers); more rows take several
-// row tiles, which read the same keys through L2.
 template <int D>
 cudaError_t launch_decode_q8(const CUtensorMap& tk, const CUtensorMap& tv,
                              const DecodeQ8Params& p, cudaStream_t stream) {
-  const long long rows = (long long)p.group * p.Lq;
-  if (rows <= 8) return launch_nb<D, 1>(tk, tv, p, stream);
-  if (rows <= 16) return launch_nb<D, 2>(tk, tv, p, stream);
-  return launch_nb<D, 4>(tk, tv, p, stream);
+  if (p.tile_rows == 8) return launch_nb<D, 1>(tk, tv, p, stream);
+  if (p.tile_rows == 16) return launch_nb<D, 2>(tk, tv, p, stream);
+  if constexpr (D == 64)
+    if (p.tile_rows == 32) return launch_nb<D, 4>(tk, tv, p, stream);
+  return cudaErrorInvalidValue;
+}
+
+// Launched so that its start overlaps the end of the decode kernel before it; it
+// waits for that kernel's results itself.
+template <int D>
+cudaError_t launch_decode_q8_combine(const DecodeQ8Params& p, cudaStream_t stream) {
+  const long long nrows = (long long)p.B * p.Hq * p.Lq;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((nrows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_decode_q8_combine_kernel<D>, p);
 }
 
 template cudaError_t launch_decode_q8<64>(const CUtensorMap&, const CUtensorMap&,
                                           const DecodeQ8Params&, cudaStream_t);
 template cudaError_t launch_decode_q8<128>(const CUtensorMap&, const CUtensorMap&,
                                            const DecodeQ8Params&, cudaStream_t);
+template cudaError_t launch_decode_q8_combine<64>(const DecodeQ8Params&, cudaStream_t);
+template cudaError_t launch_decode_q8_combine<128>(const DecodeQ8Params&, cudaStream_t);
 
-// Rows of a TMA box over the codes: a warp's unit, or a page shorter than it.
+// Rows of a TMA box over the codes: a warp's block, or a page shorter than it.
 int decode_q8_box_rows(int page_size) { return page_size < kUnit ? page_size : kUnit; }
 
 }  // namespace attn

@@ -25,13 +25,14 @@ struct CacheParams {
   int pages_per_seq, num_pages;
 };
 
-// Decode over an 8-bit cache.
+// Decode over an 8-bit cache.  The work is shared among num_ctas CTAs as q8_sched.cuh
+// describes; CTA c's partial results are slots 2 c and 2 c + 1 of the workspace.
 struct DecodeQ8Params {
   const void* q;  // bf16 [B, Hq, Lq, d]
-  void* o;        // bf16, written when nsplit == 1
-  float* lse;     // fp32, written when nsplit == 1
-  float* ws_o;    // fp32 [nsplit, B*Hq*Lq, d] otherwise
-  float* ws_lse;  // fp32 [nsplit, B*Hq*Lq]
+  void* o;        // bf16 [B, Hq, Lq, d]
+  float* lse;     // fp32 [B, Hq, Lq]
+  float* ws_o;    // fp32 [2 num_ctas, tile_rows, d]
+  float* ws_lse;  // fp32 [2 num_ctas, tile_rows]
   const uint8_t* k_exp;
   const uint8_t* v_exp;
   const int32_t* kv_lens;
@@ -39,9 +40,19 @@ struct DecodeQ8Params {
   int* err;
   int B, Hq, Hkv, Lq, Lk, group;
   float scale_log2;
-  int chunk, nsplit;
-  int row_tiles;  // row tiles per (b, kv head)
+  int num_ctas;
+  int tile_rows;  // query rows of a unit: 8, 16, 32 or 128
+  int row_tiles;  // units per (b, kv head): ceil(group * Lq / tile_rows)
   int page_size, page_shift, pages_per_seq, num_pages;
 };
+
+// Query rows per unit for `rows` query rows per KV head.  Up to 16 (32 at d = 64)
+// go through mma.m16n8k16 (attn_decode_q8.cu), the smallest of its tiles that holds
+// them; more are worth expanding the codes for tcgen05 (attn_decode_q8_wide.cu).
+inline int decode_q8_tile_rows(int d, long long rows) {
+  if (rows <= 8) return 8;
+  if (rows <= 16) return 16;
+  return d == 64 && rows <= 32 ? 32 : 128;
+}
 
 }  // namespace attn

@@ -108,7 +108,7 @@ def test_read_rejects_on_host(paged, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(q=None), INV), (dict(o=M), INV), (dict(ke=None), INV), (dict(lse=None), INV),
     (dict(Hq=15), INV), (dict(Lq=0), INV), (dict(B=0), INV), (dict(scale=0.0), INV),
-    (dict(scale=float("inf")), INV), (dict(ns=-1), INV), (dict(d=96), UNS), (dict(ws=None), WSP),
+    (dict(scale=float("inf")), INV), (dict(ns=-1), INV), (dict(ns=4097), INV), (dict(d=96), UNS), (dict(ws=None), WSP),
     (dict(wsb=64), WSP), (dict(ws=ctypes.c_void_p(0x100010)), WSP)])
 def test_decode_rejects_on_host(paged, kw, status):
     assert _decode(paged, **kw) == status
@@ -122,6 +122,21 @@ def test_bad_pages_are_rejected_on_host(call, kw, status):
 
 def test_lengths_of_a_contiguous_cache():
     assert _append(Lk=0) == INV and _read(Lk=0) == INV and _decode(Lk=0) == INV
+    assert _decode(Lk=0x7fffffff) == UNS
+
+
+def test_decode_workspace_holds_two_partials_per_cta():
+    for d, rows, tile in ((128, 8, 8), (128, 9, 16), (128, 17, 128), (64, 17, 32), (64, 33, 128),
+                          (128, 300, 128), (64, 1, 8)):
+        for ctas in (1, 7, 148):
+            part = 2 * ctas * tile
+            want = (part * d * 4 + 255) // 256 * 256 + part * 4
+            assert ab.attn_decode_q8_workspace_size(rows, 1, 1, d, ctas) == want
+    assert ab.load_library().attn_decode_q8_workspace_size(8, 3, 1, 128, 0) == 0
+    with pytest.raises(ab.AttnError):
+        ab.attn_decode_q8_workspace_size(8, 1, 1, 128, -1)
+    need = ab.attn_decode_q8_workspace_size(16, 2, 1, 128, 5)
+    assert _decode(ns=5, wsb=need - 1) == WSP
 
 
 def test_binding_rejects_host_tensors_and_missing_tables():
