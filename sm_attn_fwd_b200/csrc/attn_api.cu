@@ -1381,6 +1381,11 @@ attn_status_t decode_q8_impl(const void* q, const void* k_codes, const void* v_c
   if (Lk_max > 0x7fffffff - 4096) return ATTN_ERR_UNSUPPORTED;  // key counters are 32-bit
   if ((long long)B * Hq > 0x7fffffffLL / Lq) return ATTN_ERR_UNSUPPORTED;
   const long long nrows = (long long)B * Hq * Lq;
+  // the line of work that the CTAs share has 32-bit positions
+  const long long unit_cost = ceil_div(Lk_max, kBlockN) + attn::kQ8Piece;
+  if ((long long)B * Hkv > 0x7fffffffLL / pl.row_tiles ||
+      (long long)B * Hkv * pl.row_tiles > 0x7fffffffLL / unit_cost)
+    return ATTN_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) || ws_bytes < pl.bytes) return ATTN_ERR_WORKSPACE;
 
   attn::DecodeQ8Params p;

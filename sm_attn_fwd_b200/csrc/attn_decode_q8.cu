@@ -72,16 +72,17 @@ struct Q8Cfg {
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   // merge buffers: a warp's accumulators and statistics, one 128-byte row per register
   static constexpr int kMergeRegs = NB * (D / 16 * 4 + 6);
-  static constexpr int kMergeBytes = kWarps / 2 * kMergeRegs * 128;
+  static constexpr int kMergeBufs = kWarps == 12 ? 4 : kWarps / 2;
+  static constexpr int kMergeBytes = kMergeBufs * kMergeRegs * 128;
   static constexpr int kOffMerge = kRingBytes;
   static constexpr int kOffExp = kOffMerge + kMergeBytes;  // [warp][stage][K, V][32] scale bytes
-  static constexpr int kOffBar = kOffExp + kWarps * kStages * 64;
-  static constexpr int kOffMisc = kOffBar + kWarps * kStages * 8;
+  static constexpr int kOffQ = kOffExp + kWarps * kStages * 64;  // Q of two pieces
+  static constexpr int kOffBar = kOffQ + 2 * kRows * D * 2;
+  static constexpr int kOffMisc = kOffBar + (kWarps * kStages + 2) * 8;
   static constexpr int kSmemBytes = kOffMisc + 64;
   static constexpr int kSmemAlloc = kSmemBytes + 1024;  // slack for 1024-byte alignment
   static_assert(kSmemAlloc <= 227 * 1024, "shared memory");
-  static_assert(kWarps % 2 == 0 && kMergeBytes % 8 == 0, "merge buffers");
-};
+  };
 
 // Key of mma row g inside its group of 8 (see the head of this file).
 //   d = 128 (128-byte rows): sigma(2t + 1) = sigma(2t) ^ 4, and sigma(2t) >> 1 = t;
@@ -121,6 +122,17 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// A copy of `bytes` (a multiple of 16) from global to shared memory, both 16-byte
+// aligned, counted on the mbarrier.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(ptx::smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+      : "memory");
+}
+
 __device__ __forceinline__ void ld_shared_v2(uint32_t addr, uint32_t& a, uint32_t& b) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));
 }
@@ -151,7 +163,13 @@ __global__ void __launch_bounds__(Q8Cfg<D, NB>::kThreads, 1)
     for (int s = 0; s < S; ++s) ptx::mbar_init(&bars[s], 1);
     ptx::fence_mbar_init();
   }
+  uint64_t* q_bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + kWarps * S;
   if (warp == 0) {
+    if (lane == 0) {
+      ptx::mbar_init(&q_bars[0], 1);
+      ptx::mbar_init(&q_bars[1], 1);
+      ptx::fence_mbar_init();
+    }
     const q8::Share sh =
         q8::find_share(p.kv_lens, p.B, p.Lk, units, blockIdx.x, gridDim.x, p.err);
     if (lane == 0) {
@@ -163,6 +181,21 @@ __global__ void __launch_bounds__(Q8Cfg<D, NB>::kThreads, 1)
     ptx::prefetch_tmap(&tm_v);
   }
   __syncthreads();
+  q8::let_next_kernel_launch();
+
+  // Q of a piece, one copy of its rows (they lie one after another) into buffer
+  // piece % 2, by one thread a piece ahead.
+  const int rows_all = p.group * p.Lq;
+  int q_issued = 0;
+  auto load_q = [&](const q8::Walk& a, int piece) {
+    const int hkv = a.h / p.row_tiles, rt = a.h - hkv * p.row_tiles;
+    const long long row = ((long long)a.b * p.Hkv + hkv) * rows_all + (long long)rt * C::kRows;
+    const uint32_t bytes = (uint32_t)(min(C::kRows, rows_all - rt * C::kRows) * D * 2);
+    ptx::mbar_arrive_expect_tx(&q_bars[piece & 1], bytes);
+    bulk_load(smem + C::kOffQ + (piece & 1) * (C::kRows * D * 2),
+              reinterpret_cast<const __nv_bfloat16*>(p.q) + row * D, bytes, &q_bars[piece & 1]);
+    q_issued = piece + 1;
+  };
 
   // ------------------------------------------------------------------ loads
   uint8_t* ring = smem + warp * S * C::kStageBytes;
@@ -201,16 +234,15 @@ __global__ void __launch_bounds__(Q8Cfg<D, NB>::kThreads, 1)
   l_end = min(lw.t1 * 128, lw.len);
   find_block();
   int n_issued = 0;
-  int pend_ke = 1, pend_ve = 1;  // scale bytes of the block issued last, not stored yet
-  auto store_exps = [&]() {
-    if (n_issued == 0) return;
-    uint8_t* dst = exps + (n_issued - 1) % S * 64;
-    dst[lane] = (uint8_t)pend_ke;
-    dst[32 + lane] = (uint8_t)pend_ve;
+  // the scale bytes of block i
+  auto store_exps = [&](int i, int ke, int ve) {
+    uint8_t* dst = exps + i % S * 64;
+    dst[lane] = (uint8_t)ke;
+    dst[32 + lane] = (uint8_t)ve;
   };
   // Issue the boxes of the next block (one per operand, or one per page slice for pages
   // shorter than a block), load its scale bytes and find the block after it.
-  auto issue = [&]() {
+  auto issue = [&](int& ke, int& ve) {
     const int s = n_issued % S;
     uint8_t* kd = ring + s * C::kStageBytes;
     uint8_t* vd = kd + C::kTileBytes;
@@ -223,31 +255,42 @@ __global__ void __launch_bounds__(Q8Cfg<D, NB>::kThreads, 1)
       ptx::tma_load_3d_hint(kd + lane * D, &tm_k, &bars[s], 0, y, z, kv_policy);
       ptx::tma_load_3d_hint(vd + lane * D, &tm_v, &bars[s], 0, y, z, kv_policy);
     }
-    pend_ke = pend_ve = 1;
+    ke = ve = 1;
     const int j = l_key + lane;
     if (j < l_end && z >= 0) {
       const long long at = paged ? ((long long)z << p.page_shift) + (j & (p.page_size - 1))
                                  : (long long)z * p.Lk + j;
-      pend_ke = __ldg(p.k_exp + at);
-      pend_ve = __ldg(p.v_exp + at);
+      ke = __ldg(p.k_exp + at);
+      ve = __ldg(p.v_exp + at);
     }
     ++n_issued;
     l_key += kWarps * kUnit;
     find_block();
   };
-  for (int i = 0; i < S && lw.valid(); ++i) {
-    store_exps();
-    issue();
+  {
+    int ke[S], ve[S];  // every load goes out before the first is waited for
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+      if (lw.valid()) issue(ke[i], ve[i]);
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+      if (i < n_issued) store_exps(i, ke[i], ve[i]);
   }
+  int pend_ke = 1, pend_ve = 1;  // scale bytes of the block issued last
+  bool pending = false;          // not stored yet
 
   const int sg = sigma<D>(g), s2t0 = sigma<D>(2 * t), s2t1 = sigma<D>(2 * t + 1);
   bool ok = true;
   int done = 0;  // blocks consumed
   float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
   q8::Walk w;
-  for (w.start(*share, p.kv_lens, p.Lk); w.valid(); w.next(p.kv_lens, p.Lk, units)) {
+  w.start(*share, p.kv_lens, p.Lk);
+  if (threadIdx.x == 0 && w.valid()) load_q(w, 0);
+  for (int piece = 0; w.valid(); ++piece) {
+    q8::Walk next = w;  // the piece after this one
+    next.next(p.kv_lens, p.Lk, units);
+    if (threadIdx.x == 0 && next.valid()) load_q(next, piece + 1);
     const int hkv = w.h / p.row_tiles, rt = w.h - hkv * p.row_tiles;
-    const int rows_all = p.group * p.Lq;
     const int rows_valid = min(C::kRows, rows_all - rt * C::kRows);
     // flat output row of the unit's first row
     const long long row0 =
@@ -258,6 +301,10 @@ __global__ void __launch_bounds__(Q8Cfg<D, NB>::kThreads, 1)
     // B operand of S^T: query row n = g of each 8-row block, d in the order above
     uint32_t qf[NB][kJ * 4][2];
     float fac0[NB], fac1[NB];  // scale * log2 e * 2^(row shift) of query rows 2t and 2t + 1
+    ok = ok && ptx::mbar_wait_a(ptx::smem_u32(&q_bars[piece & 1]), (uint32_t)(piece >> 1) & 1u,
+                                abort_flag, p.err, kDevErrTimeoutProducer);
+    const uint4* q_s =
+        reinterpret_cast<const uint4*>(smem + C::kOffQ + (piece & 1) * (C::kRows * D * 2));
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       uint4 raw[kJ][2];
@@ -266,10 +313,8 @@ __global__ void __launch_bounds__(Q8Cfg<D, NB>::kThreads, 1)
       for (int j = 0; j < kJ; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          raw[j][h] = r < rows_valid
-                          ? __ldg(reinterpret_cast<const uint4*>(p.q) + (row0 + r) * (D / 8) +
-                                  j * 8 + t * 2 + h)
-                          : make_uint4(0, 0, 0, 0);
+          raw[j][h] =
+              r < rows_valid ? q_s[r * (D / 8) + j * 8 + t * 2 + h] : make_uint4(0, 0, 0, 0);
       float amax = 0.0f;
 #pragma unroll
       for (int j = 0; j < kJ; ++j)
@@ -328,8 +373,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, NB>::kThreads, 1)
                             kDevErrTimeoutProducer);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      // the bytes of the block issued last: this block's, if the ring has just started
-      store_exps();
+      if (pending) store_exps(n_issued - 1, pend_ke, pend_ve);
       __syncwarp();
       const uint32_t sk = ptx::smem_u32(ring + s * C::kStageBytes);
       const uint32_t sv = sk + C::kTileBytes;
@@ -467,35 +511,40 @@ __global__ void __launch_bounds__(Q8Cfg<D, NB>::kThreads, 1)
       // every lane has read the stage: the next block may land there
       __syncwarp();
       ++done;
-      if (lw.valid()) issue();
+      pending = lw.valid();
+      if (pending) issue(pend_ke, pend_ve);
     }
 
     // ----------------------------------------------------------------- merge
-    // Pairwise: the upper half of the warps leaves O (in units of 2^R), m, R and its
-    // lanes' parts of l in shared memory, the lower half adds them to its own; lane by
-    // lane, as every warp has the same layout.
-    ok = __syncthreads_and(ok ? 1 : 0) != 0;  // also: the buffers are free again
-    for (int n = kWarps; n > 1;) {
-      const int half = (n + 1) / 2;
-      if (warp >= half && warp < n) {
-        float* dst = merge + (warp - half) * (C::kMergeRegs * 32) + lane;
+    // Warps leave O (in units of 2^R), m, R and their lanes' parts of l in shared memory,
+    // one 128-byte row per register.  While there are more warps than buffers, the last
+    // ones' results are added to the first ones'; then all threads merge the rest
+    // and write the result.  Only warps that had a block of the piece take part.
+    auto leave = [&](int buf) {
+      float* dst = merge + buf * (C::kMergeRegs * 32) + lane;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+      for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            dst[(nb * 6 + i) * 32] = m[nb][i];
-            dst[(nb * 6 + 2 + i) * 32] = R[nb][i];
-            dst[(nb * 6 + 4 + i) * 32] = l[nb][i];
-          }
-#pragma unroll
-          for (int mu = 0; mu < kMu; ++mu)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[(NB * 6 + (nb * kMu + mu) * 4 + i) * 32] = o[nb][mu][i];
+        for (int i = 0; i < 2; ++i) {
+          dst[(nb * 6 + i) * 32] = m[nb][i];
+          dst[(nb * 6 + 2 + i) * 32] = R[nb][i];
+          dst[(nb * 6 + 4 + i) * 32] = l[nb][i];
         }
+#pragma unroll
+        for (int mu = 0; mu < kMu; ++mu)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[(NB * 6 + (nb * kMu + mu) * 4 + i) * 32] = o[nb][mu][i];
       }
+    };
+    ok = __syncthreads_and(ok ? 1 : 0) != 0;  // also: the buffers are free again
+    const int blocks = (key_end - w.t0 * 128 + kUnit - 1) / kUnit;
+    int n = min(kWarps, blocks);
+    while (n > C::kMergeBufs) {
+      const int keep = max(n - C::kMergeBufs, C::kMergeBufs);
+      if (warp >= keep && warp < n) leave(warp - keep);
       __syncthreads();
-      if (warp < n - half) {
+      if (warp < n - keep) {
         const float* src = merge + warp * (C::kMergeRegs * 32) + lane;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -520,53 +569,64 @@ __global__ void __launch_bounds__(Q8Cfg<D, NB>::kThreads, 1)
                              src[(NB * 6 + (nb * kMu + mu) * 4 + i) * 32] * a1[i & 1];
         }
       }
-      n = half;
-      if (n > 1) __syncthreads();
+      n = keep;
+      __syncthreads();
     }
-    if (warp == 0) {
-      // thread (g, t): d = (D / 8) g .. + D / 8 - 1 of query rows 2t and 2t + 1
-      const bool final = w.whole();
-      const long long at = final ? 0 : (long long)w.slot(blockIdx.x) * C::kRows;
+    if (warp < n) leave(warp);
+    __syncthreads();
+    const bool final = w.whole();
+    const long long at = final ? row0 : (long long)w.slot(blockIdx.x) * C::kRows;
+    // a warp's item: two consecutive d of rows 2t + i, i.e. registers (nb, mu, i) and
+    // (nb, mu, 2 + i) of every lane
+    for (int item = warp; item < NB * 2 * kMu; item += kWarps) {
+      const int nb = item / (2 * kMu), i = item / kMu & 1, mu = item % kMu;
+      const float* st = merge + (nb * 6 + i) * 32 + lane;
+      const float* ov = merge + (NB * 6 + (nb * kMu + mu) * 4 + i) * 32 + lane;
+      float M = -INFINITY, Rm = -INFINITY;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float ls = l[nb][i];
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
-          const int r = nb * 8 + 2 * t + i;
-          const bool have = ok && ls > 0.0f;
-          const float mu0 = m[nb][i] == -INFINITY ? 0.0f : m[nb][i];
-          const float lse = have ? (mu0 + ptx::lg2(ls)) * kLn2 : -INFINITY;
-          // O is in units of 2^R, l in units of 2^m
-          const float inv = have ? 1.0f / ls : 0.0f;
-          const float f = R[nb][i] == -INFINITY ? 0.0f : ptx::ex2(R[nb][i] - mu0);
-          float v[2 * kMu];
-#pragma unroll
-          for (int mu = 0; mu < kMu; ++mu) {
-            v[2 * mu] = o[nb][mu][i] * inv * f;
-            v[2 * mu + 1] = o[nb][mu][2 + i] * inv * f;
-          }
-          if (r >= rows_valid) continue;
-          if (final) {
-            uint4* dst = reinterpret_cast<uint4*>(p.o) + (row0 + r) * (D / 8) + g * (D / 64);
-#pragma unroll
-            for (int x = 0; x < D / 64; ++x)
-              dst[x] = make_uint4(ptx::pack_bf16x2(v[8 * x], v[8 * x + 1]),
-                                  ptx::pack_bf16x2(v[8 * x + 2], v[8 * x + 3]),
-                                  ptx::pack_bf16x2(v[8 * x + 4], v[8 * x + 5]),
-                                  ptx::pack_bf16x2(v[8 * x + 6], v[8 * x + 7]));
-            if (g == 0) p.lse[row0 + r] = lse;
-          } else {
-            float4* dst = reinterpret_cast<float4*>(p.ws_o + (at + r) * D + g * (D / 8));
-#pragma unroll
-            for (int x = 0; x < D / 32; ++x)
-              dst[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-            if (g == 0) p.ws_lse[at + r] = lse;
-          }
+      for (int x = 0; x < C::kMergeBufs; ++x)
+        if (x < n) {
+          M = fmaxf(M, st[x * C::kMergeRegs * 32]);
+          Rm = fmaxf(Rm, st[x * C::kMergeRegs * 32 + 64]);
         }
+      const float Mu = M == -INFINITY ? 0.0f : M, Ru = Rm == -INFINITY ? 0.0f : Rm;
+      float ls = 0.0f, v0 = 0.0f, v1 = 0.0f;
+#pragma unroll
+      for (int x = 0; x < C::kMergeBufs; ++x)
+        if (x < n) {
+          const int off = x * C::kMergeRegs * 32;
+          ls += st[off + 128] * ptx::ex2(st[off] - Mu);
+          const float a = ptx::ex2(st[off + 64] - Ru);
+          v0 += a * ov[off];
+          v1 += a * ov[off + 64];
+        }
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
+      const bool have = ok && ls > 0.0f;
+      const float inv = have ? 1.0f / ls : 0.0f;
+      const float f = ptx::ex2(Ru - Mu);  // O is in units of 2^R, l in units of 2^m
+      v0 = v0 * inv * f;
+      v1 = v1 * inv * f;
+      const int r = nb * 8 + 2 * t + i;
+      if (r < rows_valid) {
+        const long long to = (at + r) * D + g * (D / 8) + 2 * mu;
+        if (final)
+          *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(p.o) + to) =
+              ptx::pack_bf16x2(v0, v1);
+        else
+          *reinterpret_cast<float2*>(p.ws_o + to) = make_float2(v0, v1);
+        if (mu == 0 && g == 0)
+          (final ? p.lse : p.ws_lse)[at + r] = have ? (Mu + ptx::lg2(ls)) * kLn2 : -INFINITY;
+      }
     }
     if (!ok) break;
+    w = next;
+  }
+  if (!ok && threadIdx.x == 0) {
+    for (int i = max(0, q_issued - 2); i < q_issued; ++i) {
+      int dummy = 0;
+      ptx::mbar_wait_a(ptx::smem_u32(&q_bars[i & 1]), (uint32_t)(i >> 1) & 1u, &dummy, nullptr, 0);
+    }
   }
   if (!ok && lane == 0) {
     // a wait gave up: let the copies in flight land before the CTA goes away
@@ -605,18 +665,15 @@ __global__ void __launch_bounds__(256) attn_decode_q8_combine_kernel(const Decod
   const int units = p.Hkv * p.row_tiles;
   const int unit = (bh - b * p.Hkv) * p.row_tiles + r / p.tile_rows;
   const int rr = r % p.tile_rows;
-  // the line's tiles, and those before sequence b
-  long long all = 0, before = 0;
+  // the line's length, and what lies before sequence b
+  int all = 0, before = 0;
   for (int i = lane; i < p.B; i += 32) {
-    const int n = q8::tiles_of(q8::seq_len(p.kv_lens, i, p.Lk));
+    const int n = q8::cost_of(q8::seq_len(p.kv_lens, i, p.Lk));
     all += n;
     if (i < b) before += n;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
+  const int T = __reduce_add_sync(0xffffffffu, all) * units;
+  before = __reduce_add_sync(0xffffffffu, before) * units;
   const int tiles = q8::tiles_of(q8::seq_len(p.kv_lens, b, p.Lk));
   // every thread waits, so that whatever follows this kernel follows the one before it
   wait_for_previous_kernel();
@@ -626,15 +683,14 @@ __global__ void __launch_bounds__(256) attn_decode_q8_combine_kernel(const Decod
   for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
   float lse = -INFINITY;
   if (tiles > 0) {
-    const long long T = all * units;
-    const long long base = before * units + (long long)unit * tiles;
-    const int G = q8::ctas_used(T, p.num_ctas);
-    const long long c0 = q8::cta_of(base, T, G), c1 = q8::cta_of(base + tiles - 1, T, G);
+    const int first = before + unit * (tiles + kQ8Piece) + kQ8Piece;  // the unit's tile 0
+    const q8::Split split(T, q8::ctas_used(T, p.num_ctas));
+    const int c0 = split.of(first), c1 = split.of(first + tiles - 1);
     if (c0 == c1) return;  // written by its CTA
-    const int n = (int)(c1 - c0) + 1;
+    const int n = c1 - c0 + 1;
     // piece i of the unit: the start (slot 2 c0 + 1), then the ends and middles (2 c)
     auto slot_row = [&](int i) {
-      return (2 * (c0 + i) + (i == 0 ? 1 : 0)) * p.tile_rows + rr;
+      return (long long)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * p.tile_rows + rr;
     };
     float mx = -INFINITY;
     for (int i = lane; i < n; i += 32) mx = fmaxf(mx, p.ws_lse[slot_row(i)]);

@@ -53,8 +53,8 @@ namespace {
 
 constexpr int kThreads = 640;
 // registers per thread of the warpgroups: loads and MMAs; softmax (two); expansion of K
-// and of V.  40 + 2 * 168 + 2 * 48 <= 5 * 96, the launch's.
-constexpr int kRegsIssue = 40;
+// and of V.  48 + 2 * 168 + 2 * 48 = 5 * 96, the launch's.
+constexpr int kRegsIssue = 48;
 constexpr int kRegsExpand = 48;
 constexpr int kRegsSoftmax = 168;
 constexpr int kTmemCols = 512;
@@ -79,7 +79,7 @@ struct WCfg {
   // factors of the keys of a tile, as bf16 exponents: K's 128, then V's
   static constexpr int kOffFactor = kOffMl + 1024;
   static constexpr int kOffMisc = kOffFactor + kFactorSlots * 256;
-  static constexpr int kOffBar = kOffMisc + 40 + kRefSlots * 8;
+  static constexpr int kOffBar = kOffMisc + 32 + kRefSlots * 8;
   static constexpr int kNumBars = 12 + 2 * kFactorSlots + 4 * kRaw + 4 * kStages;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8;
   static constexpr int kSmemAlloc = kSmemBytes + 1024;
@@ -121,7 +121,7 @@ struct Misc {
   q8::Share share;
   float2 ref[kRefSlots];  // per tile: 2^(kref - 127), vref - 127
 };
-static_assert(sizeof(Misc) == 40 + kRefSlots * 8, "kOffBar");
+static_assert(sizeof(Misc) == 32 + kRefSlots * 8, "kOffBar");
 
 enum : int {
   kQFull = 0,
@@ -226,8 +226,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = misc->tmem_base;
-  const q8::Share share = misc->share;
-  const int total = (int)(share.g1 - share.g0);  // key tiles of this CTA
+  const q8::Share& share = misc->share;
+  const int total = share.tiles;
+  //q8::let_next_kernel_launch();
   bool ok = true;
 
   if (warp < 4) {
@@ -542,19 +543,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       return __all_sync(0xffffffffu, a);
     };
     int base = 0;  // tiles of the earlier pieces
-    int n = 0;     // own tiles done
-    int n_odd = 0; // odd tiles of the pieces so far
-    int piece = 0;
+    // barrier parities, in one register: own tiles done (bit 0), odd tiles of the earlier
+    // pieces (bit 1), pieces done (bit 2); bit 3: a piece is done
+    uint32_t ph = 0;
     q8::Walk w;
     for (w.start(share, p.kv_lens, p.Lk); w.valid() && ok;
-         w.next(p.kv_lens, p.Lk, units), ++piece) {
+         w.next(p.kv_lens, p.Lk, units), ph = (ph ^ 4u) | 8u) {
       const int end = base + w.t1 - w.t0;
       const int first = base + ((x ^ base) & 1);
       const int key_end = min(w.t1 * 128, w.len);
       float m_ref = -INFINITY, l = 0.0f;
-      for (int j = first; j < end; j += 2, ++n) {
+      for (int j = first; j < end; j += 2, ph ^= 1u) {
         const int left = key_end - (w.t0 + j - base) * 128;  // keys of the tile below the end
-        ok = wait(BAR(kSFull + x), (uint32_t)n & 1u);
+        ok = wait(BAR(kSFull + x), ph & 1u);
         if (!ok) break;
         ptx::tc_fence_after();
         const float2 ref = misc->ref[j % kRefSlots];
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
         if (j > first && __any_sync(0xffffffffu, need)) {
           // O holds the P V of the warpgroup's earlier tiles: final before it is rescaled
-          ok = wait(BAR(kODone + x), (uint32_t)(n - 1) & 1u);
+          ok = wait(BAR(kODone + x), ~ph & 1u);
           if (!ok) break;
           ptx::tc_fence_after();
 #pragma unroll 1
@@ -604,19 +605,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // ------------------------------------------------------- end of the piece
       const int odd = (end >> 1) - (base >> 1);  // odd tiles of the piece
-      n_odd += odd;
+      ph ^= (uint32_t)(odd & 1) << 1;
       const bool has_even = end - base > odd, has_odd = odd > 0;
       base = end;
       if (x == 1) {
-        if (piece > 0) ok = wait(BAR(kMlEmpty), (uint32_t)(piece - 1) & 1u);
+        if (ph & 8u) ok = wait(BAR(kMlEmpty), ~ph >> 2 & 1u);
         if (!ok) break;
         ml[r] = make_float2(m_ref, l);
         ptx::mbar_arrive_a(BAR(kMlFull));
         continue;
       }
-      ok = (!has_even || wait(BAR(kODone), (uint32_t)(n - 1) & 1u)) &&
-           (!has_odd || wait(BAR(kODone + 1), (uint32_t)(n_odd - 1) & 1u)) &&
-           wait(BAR(kMlFull), (uint32_t)piece & 1u);
+      ok = (!has_even || wait(BAR(kODone), ~ph & 1u)) &&
+           (!has_odd || wait(BAR(kODone + 1), ~ph >> 1 & 1u)) &&
+           wait(BAR(kMlFull), ph >> 2 & 1u);
       if (!ok) break;
       ptx::tc_fence_after();
       const float2 other = ml[r];

@@ -46,6 +46,9 @@ struct DecodeQ8Params {
   int page_size, page_shift, pages_per_seq, num_pages;
 };
 
+// Cost, in key tiles, of starting on and finishing a unit (q8_sched.cuh).
+constexpr int kQ8Piece = 3;
+
 // Query rows per unit for `rows` query rows per KV head.  Up to 16 (32 at d = 64)
 // go through mma.m16n8k16 (attn_decode_q8.cu), the smallest of its tiles that holds
 // them; more are worth expanding the codes for tcgen05 (attn_decode_q8_wide.cu).
