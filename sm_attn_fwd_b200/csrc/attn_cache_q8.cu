@@ -35,74 +35,97 @@ __device__ __forceinline__ long long cache_row(const CacheParams& p, int b, int 
   return (((long long)page * p.Hkv + h) << p.page_shift) + (j & ((1 << p.page_shift) - 1));
 }
 
-// Eight bf16 values (one 16-byte load) of a row shared by kLanes lanes -> their codes.
-template <int kLanes>
-__device__ __forceinline__ uint2 quantise8(const uint4& raw, int& e_out) {
+// The largest magnitude of eight bf16 values, as its bits (magnitudes of bf16 order
+// like their bits; 0x7f80 and above are infinity and NaN).
+__device__ __forceinline__ uint32_t max_bits(const uint4& w) {
+  const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                              __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+  return __vmaxu2(m, m >> 16) & 0xffffu;
+}
+// The same with infinities and NaN left out: they do not set a row's scale.
+__device__ __forceinline__ uint32_t max_finite_bits(const uint4& raw) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  float x[8];
-  float amax = 0.0f;
+  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+    if (lo < 0x7f80u) m = max(m, lo);
+    if (hi < 0x7f80u) m = max(m, hi);
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    // infinities and NaN do not set the scale (fmaxf drops NaN): an infinity saturates
-    const float a = fabsf(x[i]);
-    amax = fmaxf(amax, a < INFINITY ? a : 0.0f);
-  }
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1)
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const int e = q8::scale_byte(amax);
-  const float inv = q8::inv_scale_of(e);
-  e_out = e;
-  uint2 c;
-  c.x = q8::codes2(x[0] * inv, x[1] * inv) | (q8::codes2(x[2] * inv, x[3] * inv) << 16);
-  c.y = q8::codes2(x[4] * inv, x[5] * inv) | (q8::codes2(x[6] * inv, x[7] * inv) << 16);
-  return c;
+  return m;
 }
 
-// U rows per lane group, kCacheThreads / kLanes rows apart: their loads go out together.
+// Eight bf16 values times 2^(127 - e) as e4m3 codes.  The product is exact in bf16
+// (a power of two; what falls below bf16's range is far below the smallest code).
+__device__ __forceinline__ uint2 quantise8(const uint4& raw, int e) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  const uint32_t f = (uint32_t)(254 - e) << 7 | (uint32_t)(254 - e) << 23;
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&f));
+    const uint32_t b = *reinterpret_cast<const uint32_t*>(&y);
+    c[i] = q8::codes2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+  }
+  return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+}
+
+// The kernels were bound by instructions, not memory, as first written (one division
+// chain per row, fp32 maxima; 70 % of the issue slots at 1.9 TB/s), so: a block stays
+// inside one (sequence, head), whose length and page row it looks up once; the
+// maximum of a row runs on packed bf16 magnitudes; K's and V's share their shuffles.
+//
+// blockIdx.x: chunk of kGroups * U rows; blockIdx.y, z: (b, h).  U rows per lane group,
+// kGroups apart: their loads go out together.
 template <int D, int U>
 __global__ void __launch_bounds__(kCacheThreads) attn_cache_append_kernel(const CacheParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kCacheThreads / kLanes;  // rows a block takes at a time
   const int part = threadIdx.x % kLanes;
-  const int nrows = p.B * p.Hkv * p.Ln;  // at most 2^31 - 1, checked on the host
-  const long long first = (long long)blockIdx.x * (kGroups * U) + threadIdx.x / kLanes;
+  const int bh = blockIdx.z * gridDim.y + blockIdx.y;
+  if (bh >= p.B * p.Hkv) return;
+  const int b = bh / p.Hkv, h = bh - b * p.Hkv;
+  const int first = blockIdx.x * (kGroups * U) + threadIdx.x / kLanes;
+  const int len = __ldg(p.kv_lens + b);
+  const int n_new = p.new_lens ? __ldg(p.new_lens + b) : p.Ln;
+  if (len < 0 || len > p.Lk || n_new < 0 || n_new > p.Ln || n_new > len) {
+    if (first == 0 && h == 0 && part == 0) atomicOr(p.err, kDevErrBadKvLen);
+    return;  // the whole block
+  }
+  if ((int)blockIdx.x * (kGroups * U) >= n_new) return;
+  const long long in0 = (long long)bh * p.Ln * kLanes + part;  // in 16-byte units
   uint4 kr[U], vr[U];
   long long dst[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
+    const int i = first + u * kGroups;
     kr[u] = vr[u] = make_uint4(0, 0, 0, 0);
     dst[u] = -1;
-    if (first + u * kGroups >= nrows) continue;
-    const int row = (int)(first + u * kGroups);
-    const int bh = row / p.Ln, i = row - bh * p.Ln;
-    const int b = bh / p.Hkv, h = bh - b * p.Hkv;
-    const int len = __ldg(p.kv_lens + b);
-    const int n_new = p.new_lens ? __ldg(p.new_lens + b) : p.Ln;
-    if (len < 0 || len > p.Lk || n_new < 0 || n_new > p.Ln || n_new > len) {
-      if (i == 0 && h == 0 && part == 0) atomicOr(p.err, kDevErrBadKvLen);
-      continue;
+    if (i < n_new) {
+      kr[u] = __ldcs(reinterpret_cast<const uint4*>(p.k_in) + in0 + (long long)i * kLanes);
+      vr[u] = __ldcs(reinterpret_cast<const uint4*>(p.v_in) + in0 + (long long)i * kLanes);
+      dst[u] = cache_row(p, b, h, len - n_new + i);
     }
-    if (i >= n_new) continue;
-    const long long at = (long long)row * kLanes + part;  // in 16-byte units
-    kr[u] = __ldcs(reinterpret_cast<const uint4*>(p.k_in) + at);
-    vr[u] = __ldcs(reinterpret_cast<const uint4*>(p.v_in) + at);
-    dst[u] = cache_row(p, b, h, len - n_new + i);
   }
   // every lane takes part in the shuffles; a lane group is live as a whole
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    int ek, ev;
-    const uint2 kc = quantise8<kLanes>(kr[u], ek);
-    const uint2 vc = quantise8<kLanes>(vr[u], ev);
+    uint32_t m = max_bits(kr[u]) | max_bits(vr[u]) << 16;  // K's maximum, V's maximum
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (__any_sync(0xffffffffu, (m & 0xffffu) >= 0x7f80u || m >= 0x7f800000u)) {
+      m = max_finite_bits(kr[u]) | max_finite_bits(vr[u]) << 16;
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1)
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
+    const int ek = q8::scale_byte(__uint_as_float(m << 16));
+    const int ev = q8::scale_byte(__uint_as_float(m & 0xffff0000u));
     if (dst[u] >= 0) {
-      reinterpret_cast<uint2*>(p.k_codes)[dst[u] * kLanes + part] = kc;
-      reinterpret_cast<uint2*>(p.v_codes)[dst[u] * kLanes + part] = vc;
+      reinterpret_cast<uint2*>(p.k_codes)[dst[u] * kLanes + part] = quantise8(kr[u], ek);
+      reinterpret_cast<uint2*>(p.v_codes)[dst[u] * kLanes + part] = quantise8(vr[u], ev);
       if (part == 0) {
         p.k_exp[dst[u]] = (uint8_t)ek;
         p.v_exp[dst[u]] = (uint8_t)ev;
@@ -111,20 +134,42 @@ __global__ void __launch_bounds__(kCacheThreads) attn_cache_append_kernel(const 
   }
 }
 
-// 16 codes times 2^(e - 127) -> 16 bf16 values (32 bytes).  code * scale is exact
-// in fp32, so the only rounding is to bf16, and it rounds only below bf16's
-// normal range (a code has 4 significant bits).
-__device__ __forceinline__ void restore16(const uint4& c, float s, uint4 (&out)[2]) {
+// 16 codes times 2^(e - 127) -> 16 bf16 values (32 bytes).  Two codes sign-extended
+// into 16-bit halves, shifted by 4 and masked, read as bf16, are the values times
+// 2^-120; one packed multiply finishes two of them, exactly except below bf16's normal
+// range, where it rounds to nearest even.
+__device__ __forceinline__ void restore16(const uint4& c, int e, uint4 (&out)[2]) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   uint32_t r[8];
+  // 2^(e - 7); above bf16's range (e > 134) 2^120 and 2^(e - 127) one after the other
+  const uint32_t x = e <= 134 ? (uint32_t)(e + 120) : 247u;
+  const uint32_t f = x << 7 | x << 23;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t lo, hi;
-    q8::codes4_to_f16(w[i], lo, hi);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    r[2 * i] = ptx::pack_bf16x2(a.x * s, a.y * s);
-    r[2 * i + 1] = ptx::pack_bf16x2(b.x * s, b.y * s);
+  for (int i = 0; i < 8; ++i) {
+    uint32_t v;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(v) : "r"(w[i >> 1]), "r"(i & 1 ? 0xb3a2 : 0x9180));
+    v = (v << 4) & 0x87f087f0u;
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&f));
+    r[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  if (e > 134) {
+    const uint32_t f2 = (uint32_t)e << 7 | (uint32_t)e << 23;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r[i]),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&f2));
+      r[i] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+  }
+  // NaN codes (magnitude 0x7f) come back as NaN: a carry out of a byte marks them
+  const uint32_t nan = (((w[0] & 0x7f7f7f7fu) + 0x01010101u) | ((w[1] & 0x7f7f7f7fu) + 0x01010101u) |
+                        ((w[2] & 0x7f7f7f7fu) + 0x01010101u) | ((w[3] & 0x7f7f7f7fu) + 0x01010101u)) &
+                       0x80808080u;
+  if (nan) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (((w[i >> 2] >> (8 * (i & 3))) & 0x7fu) == 0x7fu) r[i >> 1] |= 0x7fffu << (16 * (i & 1));
   }
   out[0] = make_uint4(r[0], r[1], r[2], r[3]);
   out[1] = make_uint4(r[4], r[5], r[6], r[7]);
@@ -135,41 +180,39 @@ __global__ void __launch_bounds__(kCacheThreads) attn_cache_read_kernel(const Ca
   constexpr int kLanes = D / 16;
   constexpr int kGroups = kCacheThreads / kLanes;
   const int part = threadIdx.x % kLanes;
-  const int nrows = p.B * p.Hkv * p.Lk;
-  const long long first = (long long)blockIdx.x * (kGroups * U) + threadIdx.x / kLanes;
+  const int bh = blockIdx.z * gridDim.y + blockIdx.y;
+  if (bh >= p.B * p.Hkv) return;
+  const int b = bh / p.Hkv, h = bh - b * p.Hkv;
+  const int first = blockIdx.x * (kGroups * U) + threadIdx.x / kLanes;
+  const int len = __ldg(p.kv_lens + b);
+  if (len < 0 || len > p.Lk) {
+    if (first == 0 && h == 0 && part == 0) atomicOr(p.err, kDevErrBadKvLen);
+    return;
+  }
   uint4 kc[U], vc[U];
-  float ks[U], vs[U];
-  bool live[U];
+  int ke[U], ve[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
+    const int j = first + u * kGroups;
     kc[u] = vc[u] = make_uint4(0, 0, 0, 0);
-    ks[u] = vs[u] = 0.0f;
-    live[u] = false;
-    if (first + u * kGroups >= nrows) continue;
-    const int row = (int)(first + u * kGroups);
-    const int bh = row / p.Lk, j = row - bh * p.Lk;
-    const int b = bh / p.Hkv, h = bh - b * p.Hkv;
-    const int len = __ldg(p.kv_lens + b);
-    if (len < 0 || len > p.Lk) {
-      if (j == 0 && h == 0 && part == 0) atomicOr(p.err, kDevErrBadKvLen);
-      continue;
-    }
+    ke[u] = ve[u] = 1;
     if (j >= len) continue;
-    live[u] = true;
     const long long src = cache_row(p, b, h, j);
     if (src < 0) continue;  // reads as zeros
     kc[u] = __ldcs(reinterpret_cast<const uint4*>(p.k_codes) + src * kLanes + part);
     vc[u] = __ldcs(reinterpret_cast<const uint4*>(p.v_codes) + src * kLanes + part);
-    ks[u] = q8::scale_of(__ldg(p.k_exp + src));
-    vs[u] = q8::scale_of(__ldg(p.v_exp + src));
+    ke[u] = __ldg(p.k_exp + src);
+    ve[u] = __ldg(p.v_exp + src);
   }
+  const long long out0 = ((long long)bh * p.Lk * kLanes + part) * 2;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    if (!live[u]) continue;
+    const int j = first + u * kGroups;
+    if (j >= len) continue;
     uint4 ko[2], vo[2];
-    restore16(kc[u], ks[u], ko);
-    restore16(vc[u], vs[u], vo);
-    const long long dst = ((first + u * kGroups) * kLanes + part) * 2;
+    restore16(kc[u], ke[u], ko);
+    restore16(vc[u], ve[u], vo);
+    const long long dst = out0 + (long long)j * (kLanes * 2);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       __stcs(reinterpret_cast<uint4*>(p.k_out) + dst + i, ko[i]);
@@ -183,9 +226,12 @@ __global__ void __launch_bounds__(kCacheThreads) attn_cache_read_kernel(const Ca
 constexpr int kRowsPerGroup = 4;
 bool many_rows(long long rows, int lanes) { return rows * lanes > 2LL * 148 * 2048; }
 
-unsigned blocks_for(long long rows, int lanes, int u) {
-  const long long per = (long long)(kCacheThreads / lanes) * u;
-  return (unsigned)((rows + per - 1) / per);
+// Chunks of `rows` rows by (b, h) pairs, the pairs in y and z (each at most 65535).
+dim3 cache_grid(int rows, int lanes, int u, long long pairs) {
+  const int per = kCacheThreads / lanes * u;
+  const long long y = pairs < 65535 ? pairs : 65535;
+  return dim3((unsigned)((rows + (long long)per - 1) / per), (unsigned)y,
+              (unsigned)((pairs + y - 1) / y));
 }
 
 }  // namespace
@@ -193,22 +239,26 @@ unsigned blocks_for(long long rows, int lanes, int u) {
 template <int D>
 cudaError_t launch_cache_append(const CacheParams& p, cudaStream_t stream) {
   constexpr int kLanes = D / 8, U = kRowsPerGroup;
-  const long long rows = (long long)p.B * p.Hkv * p.Ln;
-  if (many_rows(rows, kLanes))
-    attn_cache_append_kernel<D, U><<<blocks_for(rows, kLanes, U), kCacheThreads, 0, stream>>>(p);
+  const long long pairs = (long long)p.B * p.Hkv;
+  if (many_rows(pairs * p.Ln, kLanes))
+    attn_cache_append_kernel<D, U>
+        <<<cache_grid(p.Ln, kLanes, U, pairs), kCacheThreads, 0, stream>>>(p);
   else
-    attn_cache_append_kernel<D, 1><<<blocks_for(rows, kLanes, 1), kCacheThreads, 0, stream>>>(p);
+    attn_cache_append_kernel<D, 1>
+        <<<cache_grid(p.Ln, kLanes, 1, pairs), kCacheThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_cache_read(const CacheParams& p, cudaStream_t stream) {
   constexpr int kLanes = D / 16, U = kRowsPerGroup;
-  const long long rows = (long long)p.B * p.Hkv * p.Lk;
-  if (many_rows(rows, kLanes))
-    attn_cache_read_kernel<D, U><<<blocks_for(rows, kLanes, U), kCacheThreads, 0, stream>>>(p);
+  const long long pairs = (long long)p.B * p.Hkv;
+  if (many_rows(pairs * p.Lk, kLanes))
+    attn_cache_read_kernel<D, U>
+        <<<cache_grid(p.Lk, kLanes, U, pairs), kCacheThreads, 0, stream>>>(p);
   else
-    attn_cache_read_kernel<D, 1><<<blocks_for(rows, kLanes, 1), kCacheThreads, 0, stream>>>(p);
+    attn_cache_read_kernel<D, 1>
+        <<<cache_grid(p.Lk, kLanes, 1, pairs), kCacheThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int hkv = idx / p.nsplit;
   const bool has_b = 2 * pair + 1 < p.tiles;
   const int n_x = has_b ? 2 : 1;
+  const int n_mma = C::kSepP ? n_x : 1;  // warps issuing MMAs
   const int c0 = split * p.chunk;
   const int key_end = min(c0 + p.chunk, p.Lp);
   const int n_tiles = (key_end - c0 + 127) / 128;  // >= 1
@@ -138,12 +139,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&bars[kODone + x], 1);
       ptx::mbar_init(&bars[kTurn + x], 128);
     }
-    ptx::mbar_init(&bars[kDrain], n_x);
+    ptx::mbar_init(&bars[kDrain], n_mma);
     for (int st = 0; st < S; ++st) {
       ptx::mbar_init(&bars[kKv + st], 1);
-      ptx::mbar_init(&bars[kKv + S + st], n_x);
+      ptx::mbar_init(&bars[kKv + S + st], n_mma);
       ptx::mbar_init(&bars[kKv + 2 * S + st], 1);
-      ptx::mbar_init(&bars[kKv + 3 * S + st], n_x);
+      ptx::mbar_init(&bars[kKv + 3 * S + st], n_mma);
     }
     misc->abort = 0;
     ptx::fence_mbar_init();
@@ -244,59 +245,83 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (jj < j) ptx::mbar_wait_a(V_FULL(jj % S), ph, &dummy, nullptr, 0);
         }
       }
-    } else if (warp == 1 || (warp == 2 && has_b)) {
-      // ------------------------------------------- MMA issuer of query tile x
-      // The whole warp runs the loop; elect.sync picks the lane that issues.
-      const int x = warp - 1;
+    } else if (warp == 1 || (warp == 2 && n_mma == 2)) {
+      // ------------------------------------------------------- MMA issuers
+      // The whole warp runs the loop; elect.sync picks the lane that issues.  d = 64:
+      // one warp per query tile; d = 128: one for both (with two the 32K-key prefix of 512 rows took 101 us instead of 83).
       constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(128, 128, 0, 0);
       constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(128, D, 0, 1);
-      const uint32_t s_tmem = tmem + (x ? 128u : 0u);
-      const uint32_t p_tmem = C::kSepP ? tmem + 384u + (uint32_t)(x * 64) : s_tmem;
-      const uint32_t o_tmem = tmem + 256u + (uint32_t)(x * D);
-      const uint64_t q_desc = ptx::smem_desc_sw128(sq + x * C::kTileBytes, 16, 1024);
       auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
         const bool w = ptx::mbar_wait_a(bar, parity, abort_flag, err, kDevErrTimeoutMma);
         return __all_sync(0xffffffffu, w);
       };
-      auto issue_s = [&](int j) -> bool {
-        const int st = j % S;
-        if (!wait(K_FULL(st), (uint32_t)(j / S) & 1u)) return false;
+      auto k_ready = [&](int j) -> bool {
+        const bool w = wait(K_FULL(j % S), (uint32_t)(j / S) & 1u);
         ptx::tc_fence_after();
-        const uint64_t k_desc = ptx::smem_desc_sw128(sk + st * C::kTileBytes, 16, 1024);
+        return w;
+      };
+      // S_x = Q_x K_j^T; K_j has landed
+      auto issue_s = [&](int j, int x) {
+        const uint32_t s_tmem = tmem + (x ? 128u : 0u);
+        const uint64_t q_desc = ptx::smem_desc_sw128(sq + x * C::kTileBytes, 16, 1024);
+        const uint64_t k_desc = ptx::smem_desc_sw128(sk + j % S * C::kTileBytes, 16, 1024);
         if constexpr (D == 64)
           ptx::mma_qk_chain_d64(s_tmem, q_desc, k_desc, kIdescS);
         else
           ptx::mma_qk_chain_d128(s_tmem, q_desc, k_desc, kIdescS);
         ptx::mma_commit_warp(BAR(kSFull + x));
-        ptx::mma_commit_warp(K_EMPTY(st));
-        return true;
       };
-      auto issue_pv = [&](int j) -> bool {
+      // O_x += P_x V_j once P_x is written and V_j has landed
+      auto issue_pv = [&](int j, int x) -> bool {
         const int st = j % S;
         if (!wait(BAR(kPFull + x), (uint32_t)j & 1u)) return false;
         if (!wait(V_FULL(st), (uint32_t)(j / S) & 1u)) return false;
         ptx::tc_fence_after();
-        ptx::mma_pv_chain8(o_tmem, p_tmem,
+        const uint32_t p_tmem = tmem + (C::kSepP ? 384u + (uint32_t)(x * 64) : x ? 128u : 0u);
+        ptx::mma_pv_chain8(tmem + 256u + (uint32_t)(x * D), p_tmem,
                            ptx::smem_desc_sw128(sv_ + st * C::kTileBytes, C::kAtomBytes, 1024),
                            kIdescPV, j > 0 ? 1u : 0u);
         ptx::mma_commit_warp(BAR(kODone + x));
-        ptx::mma_commit_warp(V_EMPTY(st));
         return true;
       };
-      bool ok = wait(BAR(kQFull + x), 0);
-      if (ok) ok = issue_s(0);
-      for (int j = 0; j < n_tiles && ok; ++j) {
-        if constexpr (C::kSepP) {
+      bool ok = true;
+      if constexpr (C::kSepP) {
+        const int x = warp - 1;
+        ok = wait(BAR(kQFull + x), 0) && k_ready(0);
+        if (ok) {
+          issue_s(0, x);
+          ptx::mma_commit_warp(K_EMPTY(0));
+        }
+        for (int j = 0; j < n_tiles && ok; ++j) {
           // the next S needs S_x loaded; this tile's P V follows when P_x is written
           if (j + 1 < n_tiles) {
-            ok = wait(BAR(kSFree + x), (uint32_t)j & 1u);
-            if (ok) ok = issue_s(j + 1);
+            ok = wait(BAR(kSFree + x), (uint32_t)j & 1u) && k_ready(j + 1);
+            if (!ok) break;
+            issue_s(j + 1, x);
+            ptx::mma_commit_warp(K_EMPTY((j + 1) % S));
           }
-          if (ok) ok = issue_pv(j);
-        } else {
-          // the next S overwrites P_x: right behind this tile's P V, in pipe order
-          ok = issue_pv(j);
-          if (ok && j + 1 < n_tiles) ok = issue_s(j + 1);
+          ok = issue_pv(j, x);
+          if (ok) ptx::mma_commit_warp(V_EMPTY(j % S));
+        }
+      } else {
+        for (int x = 0; x < n_x && ok; ++x) ok = wait(BAR(kQFull + x), 0);
+        ok = ok && k_ready(0);
+        if (ok) {
+          for (int x = 0; x < n_x; ++x) issue_s(0, x);
+          ptx::mma_commit_warp(K_EMPTY(0));
+        }
+        for (int j = 0; j < n_tiles && ok; ++j) {
+          for (int x = 0; x < n_x && ok; ++x) {
+            // the next S overwrites P_x: right behind this tile's P V, in pipe order
+            ok = issue_pv(j, x);
+            if (ok && j + 1 < n_tiles) {
+              if (x == 0) ok = k_ready(j + 1);
+              if (ok) issue_s(j + 1, x);
+            }
+          }
+          if (!ok) break;
+          ptx::mma_commit_warp(V_EMPTY(j % S));
+          if (j + 1 < n_tiles) ptx::mma_commit_warp(K_EMPTY((j + 1) % S));
         }
       }
       ptx::mma_commit_warp(BAR(kDrain));

@@ -156,6 +156,36 @@ def test_read_back_is_exact_and_leaves_the_rest(case):
         assert torch.equal(got.cpu().view(torch.int16), w.view(torch.int16))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_codes_read_back_as_nan(d):
+    code, e, val = quantise(rows(13, (1, 1, 5, d)))
+    code[0, 0, 2, 7], code[0, 0, 2, d - 1], code[0, 0, 4, 0] = 0x7F, 0xFF, 0x7F
+    want = torch.from_numpy(val).to(torch.bfloat16)
+    want[0, 0, 2, 7] = want[0, 0, 2, d - 1] = want[0, 0, 4, 0] = math.nan
+    c, x = as_codes(code).cuda(), torch.from_numpy(e).cuda()
+    k, v = ab.attn_cache_read_q8(c, c, x, x, torch.tensor([5], dtype=torch.int32, device="cuda"))
+    dev_ok()
+    for got in (k, v):
+        assert torch.equal(got.cpu().isnan(), want.isnan())
+        assert torch.equal(got.cpu().nan_to_num(0.0), want.nan_to_num(0.0))
+
+
+def test_more_pairs_than_a_grid_dimension_holds():
+    """70,000 (sequence, head) pairs of one key each: written, and read back."""
+    B, d = 70000, 64
+    k = rows(14, (B, 1, 1, d))
+    code, e, val = quantise(k)
+    cv = [torch.zeros(B, 1, 1, d, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    ex = [torch.zeros(B, 1, 1, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    kv = torch.ones(B, dtype=torch.int32, device="cuda")
+    args = [c.view(torch.float8_e4m3fn) for c in cv] + ex
+    ab.attn_cache_append_q8(k.cuda(), k.cuda(), *args, kv)
+    kr, vr = ab.attn_cache_read_q8(*args, kv)
+    dev_ok()
+    assert np.array_equal(cv[0].cpu().numpy(), code) and np.array_equal(ex[1].cpu().numpy(), e)
+    assert np.array_equal(kr.cpu().double().numpy(), val) and torch.equal(kr, vr)
+
+
 def test_out_of_range_lengths_and_pages_are_skipped_and_flagged():
     B, Hkv, Ln, Lk, d = 4, 2, 3, 16, 64
     k = rows(21, (B, Hkv, Ln, d)).cuda()
