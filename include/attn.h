@@ -384,9 +384,8 @@ attn_status_t attn_decode_paged_score_mod(const void* q, const void* k_pages, co
  * 0 lets the library choose.  Returns -1 for invalid arguments.
  *
  * attn_decode_shared_prefix_workspace_size — bytes of caller workspace it needs:
- * the partials of the prefix's splits, then those of the sequences' own caches
- * (split as attn_decode_splitkv does with num_splits = 0), laid out as
- * attn_decode_workspace_size describes.  0 for invalid arguments.
+ * the partials of the prefix's splits and of the sequences' own caches.  0 for
+ * invalid arguments.
  */
 int attn_decode_shared_prefix_num_splits(int B, int Hq, int Hkv, int Lq, int Lp, int num_splits,
                                          int* chunk_keys);

@@ -18,11 +18,11 @@ CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libattn_b200.so")
 SOURCES = ["attn_api.cu", "attn_kernels.cu", "attn_prefill.cu", "attn_short.cu", "attn_noalloc.cu",
-           "attn_backward.cu", "attn_cache_q8.cu", "attn_decode_q8.cu",
+           "attn_backward.cu", "attn_cache_q8.cu", "attn_decode_rows.cu",
            "attn_decode_q8_wide.cu", "attn_prefix.cu"]
 HEADERS = ["attn_params.h", "attn_bwd_params.h", "ptx.cuh", "host_once.h", "prefill_common.cuh",
-           "softmax_row.cuh", "cache_q8.cuh", "cache_q8_params.h",
-           "attn_prefix_params.h", "q8_sched.cuh"]
+           "softmax_row.cuh", "cache_q8.cuh", "decode_params.h",
+           "attn_prefix_params.h", "decode_sched.cuh"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",

@@ -15,7 +15,7 @@
 #include "attn_bwd_params.h"
 #include "attn_params.h"
 #include "attn_prefix_params.h"
-#include "cache_q8_params.h"
+#include "decode_params.h"
 #include "host_once.h"
 
 namespace attn {
@@ -41,15 +41,15 @@ template <int D>
 cudaError_t launch_cache_append(const CacheParams&, cudaStream_t);
 template <int D>
 cudaError_t launch_cache_read(const CacheParams&, cudaStream_t);
-template <int D>
-cudaError_t launch_decode_q8(const CUtensorMap&, const CUtensorMap&, const DecodeQ8Params&,
-                             cudaStream_t);
-int decode_q8_box_rows(int page_size);
+template <int D, bool kQ8>
+cudaError_t launch_decode_rows(const CUtensorMap&, const CUtensorMap&, const DecodeParams&,
+                               cudaStream_t);
+int decode_rows_box(int d, bool q8, int page_size);
 template <int D>
 cudaError_t launch_decode_q8_wide(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
-                                  const DecodeQ8Params&, cudaStream_t);
+                                  const DecodeParams&, cudaStream_t);
 template <int D>
-cudaError_t launch_decode_q8_combine(const DecodeQ8Params&, cudaStream_t);
+cudaError_t launch_decode_merge(const DecodeParams&, cudaStream_t);
 template <int D>
 cudaError_t launch_prefix(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
                           const PrefixParams&, cudaStream_t);
@@ -909,17 +909,18 @@ void set_decode_shape(FwdParams* p, const int32_t* kv_lens, int B, int Hq, int H
 }
 
 // Tensor maps of a bf16 K/V cache: contiguous [planes, rows, d] or a page pool,
-// boxes of at most 128 rows.
+// boxes of at most box_rows rows.
 bool encode_kv(CUtensorMap* tk, CUtensorMap* tv, const void* k, const void* v, int d,
-               uint64_t rows, uint64_t planes, const PagedKv& pg, int Hkv) {
+               uint64_t rows, uint64_t planes, const PagedKv& pg, int Hkv,
+               int box_rows = kBlockN) {
   if (pg.block_table) {
     const uint64_t dk[3] = {(uint64_t)d, (uint64_t)pg.page_size,
                             (uint64_t)pg.num_pages * (uint64_t)Hkv};
-    const int box = pg.page_size < kBlockN ? pg.page_size : kBlockN;
+    const int box = std::min(pg.page_size, box_rows);
     return encode_bf16(tk, k, 3, dk, box) && encode_bf16(tv, v, 3, dk, box);
   }
   const uint64_t dk[3] = {(uint64_t)d, rows, planes};
-  return encode_bf16(tk, k, 3, dk) && encode_bf16(tv, v, 3, dk);
+  return encode_bf16(tk, k, 3, dk, box_rows) && encode_bf16(tv, v, 3, dk, box_rows);
 }
 
 // The partial kernel of the split-KV decode for launch parameters p.
@@ -1070,6 +1071,74 @@ attn_status_t attn_decode_paged_score_mod(const void* q, const void* k_pages, co
 
 }  // extern "C"
 
+// ------------------------------------------- decodes with shared-out work
+namespace {
+
+int log2_of(int pow2) {
+  int s = 0;
+  while ((1 << s) < pow2) ++s;
+  return s;
+}
+
+// CTAs among which a decode's key tiles are shared out (one per SM unless the caller
+// asks for a number), and its workspace: two partial results per CTA.
+constexpr int kMaxDecodeCtas = 4096;
+
+struct SharePlan {
+  int num_ctas, tile_rows, row_tiles;
+  size_t part_rows;       // rows of partial results
+  size_t lse_off, bytes;  // workspace: O, then the LSEs
+};
+
+bool plan_share(int Hq, int Hkv, int Lq, int d, int num_ctas, SharePlan* pl) {
+  if (Hq < 1 || Hkv < 1 || Lq < 1 || d < 1 || Hq % Hkv) return false;
+  if (num_ctas < 0 || num_ctas > kMaxDecodeCtas) return false;
+  const long long rows = (long long)(Hq / Hkv) * Lq;
+  pl->num_ctas = num_ctas > 0 ? num_ctas : num_sms();
+  pl->tile_rows = attn::decode_tile_rows(d, rows);
+  const long long tiles = ceil_div(rows, pl->tile_rows);
+  if (tiles * Hkv > 0x7fffffffLL) return false;
+  pl->row_tiles = (int)tiles;
+  pl->part_rows = 2 * (size_t)pl->num_ctas * (size_t)pl->tile_rows;
+  pl->lse_off = (pl->part_rows * (size_t)d * 4 + 255) / 256 * 256;
+  pl->bytes = pl->lse_off + pl->part_rows * 4;
+  return true;
+}
+
+// Launch parameters of such a decode except its outputs, workspace and scale bytes;
+// false for sizes whose 32-bit counters (output rows, keys, the line of work) overflow.
+bool set_share_shape(attn::DecodeParams* p, const void* q, const int32_t* kv_lens, int B, int Hq,
+                     int Hkv, int Lq, int Lk_max, float scale, const SharePlan& pl,
+                     const PagedKv& pg) {
+  if (Lk_max > 0x7fffffff - 4096) return false;
+  if ((long long)B * Hq > 0x7fffffffLL / Lq) return false;
+  const long long unit_cost = ceil_div(Lk_max, kBlockN) + attn::kPieceTiles;
+  if ((long long)B * Hkv > 0x7fffffffLL / pl.row_tiles ||
+      (long long)B * Hkv * pl.row_tiles > 0x7fffffffLL / unit_cost)
+    return false;
+  std::memset(p, 0, sizeof *p);
+  p->q = q;
+  p->kv_lens = kv_lens;
+  p->block_table = pg.block_table;
+  p->B = B;
+  p->Hq = Hq;
+  p->Hkv = Hkv;
+  p->Lq = Lq;
+  p->Lk = Lk_max;
+  p->group = Hq / Hkv;
+  p->scale_log2 = (float)((double)scale * 1.4426950408889634074);
+  p->num_ctas = pl.num_ctas;
+  p->tile_rows = pl.tile_rows;
+  p->row_tiles = pl.row_tiles;
+  p->page_size = pg.page_size;
+  p->page_shift = pg.block_table ? log2_of(pg.page_size) : 0;
+  p->pages_per_seq = pg.pages_per_seq;
+  p->num_pages = pg.num_pages;
+  return true;
+}
+
+}  // namespace
+
 // ------------------------------------------------------- shared prefix
 namespace {
 
@@ -1117,22 +1186,34 @@ bool plan_prefix(int B, int Hq, int Hkv, int Lq, int Lp, int num_splits, PrefixP
   return true;
 }
 
+// The whole call.  The sequences' own caches: with few query rows per KV head the
+// decode that shares its key tiles out (share), else the split-KV decode (split).
+// Workspace: fp32 partial outputs, the prefix's np splits first, then one row per
+// output row and two partial results per CTA (share) or the splits' (split); then, 256-byte
+// aligned, their LSEs in the same order.
 struct PrefixCall {
   PrefixPlan pp;
-  SplitPlan pl;  // of the sequences' own caches
+  bool few_rows;
+  SharePlan share;
+  SplitPlan split;
   long long nrows;
-  size_t bytes;
+  size_t part_rows;  // rows of partial results
+  size_t lse_off, bytes;
 };
 
 bool plan_prefix_call(int B, int Hq, int Hkv, int Lq, int Lp, int Lk_max, int d, int num_splits,
                       PrefixCall* pc) {
   if (!plan_prefix(B, Hq, Hkv, Lq, Lp, num_splits, &pc->pp)) return false;
-  if (!plan_splits(B, Hq, Hkv, Lq, Lk_max, d, 0, &pc->pl)) return false;
+  if (!plan_share(Hq, Hkv, Lq, d, 0, &pc->share)) return false;
+  if (!plan_splits(B, Hq, Hkv, Lq, Lk_max, d, 0, &pc->split)) return false;
   if ((long long)B * Hq > 0x7fffffffLL / Lq) return false;
   pc->nrows = (long long)B * Hq * Lq;
-  SplitPlan all = pc->pl;
-  all.nsplit += pc->pp.np;
-  pc->bytes = ws_lse_offset(all, pc->nrows, d) + (size_t)all.nsplit * (size_t)pc->nrows * 4;
+  pc->few_rows = pc->share.tile_rows < kBlockM;
+  const size_t n = (size_t)pc->nrows;
+  pc->part_rows = pc->few_rows ? (pc->pp.np + 1) * n + pc->share.part_rows
+                               : ((size_t)pc->pp.np + pc->split.nsplit) * n;
+  pc->lse_off = (pc->part_rows * (size_t)d * 4 + 255) / 256 * 256;
+  pc->bytes = pc->lse_off + pc->part_rows * 4;
   return true;
 }
 
@@ -1155,24 +1236,23 @@ attn_status_t shared_prefix_impl(const void* q, const void* k_prefix, const void
   PrefixCall pc;
   if (!plan_prefix_call(B, Hq, Hkv, Lq, Lp, Lk_max, d, num_splits, &pc))
     return ATTN_ERR_UNSUPPORTED;
-  if (pc.pl.chunk / kBlockN > attn::kMaxKvTiles) return ATTN_ERR_UNSUPPORTED;
-  if ((long long)B * Hkv * pc.pl.row_tiles > kMaxGridY) return ATTN_ERR_UNSUPPORTED;
+  attn::DecodeParams sh;
+  if (pc.few_rows) {
+    if (!set_share_shape(&sh, q, kv_lens, B, Hq, Hkv, Lq, Lk_max, scale, pc.share, pg))
+      return ATTN_ERR_UNSUPPORTED;
+  } else {
+    if (pc.split.chunk / kBlockN > attn::kMaxKvTiles) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)B * Hkv * pc.split.row_tiles > kMaxGridY) return ATTN_ERR_UNSUPPORTED;
+  }
   if ((long long)Hkv * pc.pp.pairs * pc.pp.np > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) || ws_bytes < pc.bytes) return ATTN_ERR_WORKSPACE;
   int* err = error_word_for_current_device();
   if (!err) return ATTN_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int np = pc.pp.np, G = Hq / Hkv * Lq;
-  SplitPlan all = pc.pl;
-  all.nsplit += np;
-
-  // partials: splits [0, np) the prefix, [np, np + nsplit) the sequences' own caches
-  FwdParams p;
-  std::memset(&p, 0, sizeof p);
-  set_decode_shape(&p, kv_lens, B, Hq, Hkv, Lq, Lk_max, scale, pc.pl, pg);
+  const size_t n = (size_t)pc.nrows;
   float* ws_o = reinterpret_cast<float*>(workspace);
-  float* ws_lse = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) +
-                                           ws_lse_offset(all, pc.nrows, d));
+  float* ws_lse = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + pc.lse_off);
   attn::PrefixParams x;
   std::memset(&x, 0, sizeof x);
   x.ws_o = ws_o;
@@ -1193,7 +1273,7 @@ attn_status_t shared_prefix_impl(const void* q, const void* k_prefix, const void
   x.nsplit = np;
   x.page_size = pg.page_size;
   x.num_pages = pg.num_pages;
-  x.scale_log2 = p.scale_log2;
+  x.scale_log2 = (float)((double)scale * 1.4426950408889634074);
   CUtensorMap tq, tk, tv;
   if (!encode_bf16_rows(&tq, q, d, G, Hkv, B, std::min(G, kBlockM), pc.pp.nb)) return ATTN_ERR_CUDA;
   if (!encode_kv(&tk, &tv, k_prefix, v_prefix, d, (uint64_t)Lp, (uint64_t)Hkv, pg, Hkv))
@@ -1202,16 +1282,41 @@ attn_status_t shared_prefix_impl(const void* q, const void* k_prefix, const void
                           : attn::launch_prefix<128>(tq, tk, tv, x, st);
   if (e != cudaSuccess) return ATTN_ERR_CUDA;
 
-  p.ws_o = ws_o + (size_t)np * (size_t)pc.nrows * d;
-  p.ws_lse = ws_lse + (size_t)np * (size_t)pc.nrows;
+  if (pc.few_rows) {
+    sh.o = o;
+    sh.lse = lse;
+    sh.prefix_o = ws_o;
+    sh.prefix_lse = ws_lse;
+    sh.num_prefix = np;
+    sh.own_o = ws_o + np * n * d;
+    sh.own_lse = ws_lse + np * n;
+    sh.ws_o = sh.own_o + n * d;
+    sh.ws_lse = sh.own_lse + n;
+    sh.err = err;
+    CUtensorMap ck, cv;
+    if (!encode_kv(&ck, &cv, k_cache, v_cache, d, (uint64_t)Lk_max, (uint64_t)B * Hkv, pg, Hkv,
+                   attn::decode_rows_box(d, false, kBlockN)))
+      return ATTN_ERR_CUDA;
+    e = d == 64 ? attn::launch_decode_rows<64, false>(ck, cv, sh, st)
+                : attn::launch_decode_rows<128, false>(ck, cv, sh, st);
+    if (e != cudaSuccess) return ATTN_ERR_CUDA;
+    e = d == 64 ? attn::launch_decode_merge<64>(sh, st) : attn::launch_decode_merge<128>(sh, st);
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  }
+
+  // partials: splits [0, np) the prefix, [np, np + nsplit) the sequences' own caches
+  FwdParams p;
+  std::memset(&p, 0, sizeof p);
+  set_decode_shape(&p, kv_lens, B, Hq, Hkv, Lq, Lk_max, scale, pc.split, pg);
+  p.ws_o = ws_o + np * n * d;
+  p.ws_lse = ws_lse + np * n;
   const attn_status_t ds = launch_split_decode(p, q, k_cache, v_cache, d, pg, st);
   if (ds != ATTN_OK) return ds;
-
   p.o = o;
   p.lse = lse;
   p.ws_o = ws_o;
   p.ws_lse = ws_lse;
-  p.nsplit = all.nsplit;
+  p.nsplit = np + pc.split.nsplit;
   e = d == 64 ? attn::launch_combine<64>(p, st) : attn::launch_combine<128>(p, st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
@@ -1266,12 +1371,6 @@ attn_status_t attn_decode_shared_prefix_paged(
 
 // ------------------------------------------------------- 8-bit KV cache
 namespace {
-
-int log2_of(int pow2) {
-  int s = 0;
-  while ((1 << s) < pow2) ++s;
-  return s;
-}
 
 // Arguments shared by append and read-back.
 attn_status_t cache_params(const void* k_codes, const void* v_codes, const uint8_t* k_exp,
@@ -1340,30 +1439,6 @@ attn_status_t read_impl(const void* k_codes, const void* v_codes, const uint8_t*
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// CTAs of the 8-bit decode (one per SM unless the caller asks for a number), and its
-// workspace: two partial results per CTA.
-constexpr int kMaxQ8Ctas = 4096;
-
-struct Q8Plan {
-  int num_ctas, tile_rows, row_tiles;
-  size_t lse_off, bytes;
-};
-
-bool plan_q8(int Hq, int Hkv, int Lq, int d, int num_ctas, Q8Plan* pl) {
-  if (Hq < 1 || Hkv < 1 || Lq < 1 || d < 1 || Hq % Hkv) return false;
-  if (num_ctas < 0 || num_ctas > kMaxQ8Ctas) return false;
-  const long long rows = (long long)(Hq / Hkv) * Lq;
-  pl->num_ctas = num_ctas > 0 ? num_ctas : num_sms();
-  pl->tile_rows = attn::decode_q8_tile_rows(d, rows);
-  const long long tiles = ceil_div(rows, pl->tile_rows);
-  if (tiles * Hkv > 0x7fffffffLL) return false;
-  pl->row_tiles = (int)tiles;
-  const size_t part_rows = 2 * (size_t)pl->num_ctas * (size_t)pl->tile_rows;
-  pl->lse_off = (part_rows * (size_t)d * 4 + 255) / 256 * 256;
-  pl->bytes = pl->lse_off + part_rows * 4;
-  return true;
-}
-
 attn_status_t decode_q8_impl(const void* q, const void* k_codes, const void* v_codes,
                              const uint8_t* k_exp, const uint8_t* v_exp, void* o, float* lse,
                              const int32_t* kv_lens, int B, int Hq, int Hkv, int Lq, int Lk_max,
@@ -1375,44 +1450,20 @@ attn_status_t decode_q8_impl(const void* q, const void* k_codes, const void* v_c
       !aligned(lse, 4) || !aligned(kv_lens, 4))
     return ATTN_ERR_INVALID_ARG;
   if (!(scale > 0.0f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
-  Q8Plan pl;
-  if (B < 1 || Lk_max < 1 || !plan_q8(Hq, Hkv, Lq, d, num_ctas, &pl)) return ATTN_ERR_INVALID_ARG;
+  SharePlan pl;
+  if (B < 1 || Lk_max < 1 || !plan_share(Hq, Hkv, Lq, d, num_ctas, &pl))
+    return ATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
-  if (Lk_max > 0x7fffffff - 4096) return ATTN_ERR_UNSUPPORTED;  // key counters are 32-bit
-  if ((long long)B * Hq > 0x7fffffffLL / Lq) return ATTN_ERR_UNSUPPORTED;
-  const long long nrows = (long long)B * Hq * Lq;
-  // the line of work that the CTAs share has 32-bit positions
-  const long long unit_cost = ceil_div(Lk_max, kBlockN) + attn::kQ8Piece;
-  if ((long long)B * Hkv > 0x7fffffffLL / pl.row_tiles ||
-      (long long)B * Hkv * pl.row_tiles > 0x7fffffffLL / unit_cost)
+  attn::DecodeParams p;
+  if (!set_share_shape(&p, q, kv_lens, B, Hq, Hkv, Lq, Lk_max, scale, pl, pg))
     return ATTN_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) || ws_bytes < pl.bytes) return ATTN_ERR_WORKSPACE;
-
-  attn::DecodeQ8Params p;
-  std::memset(&p, 0, sizeof p);
-  p.q = q;
   p.o = o;
   p.lse = lse;
   p.ws_o = reinterpret_cast<float*>(workspace);
   p.ws_lse = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + pl.lse_off);
   p.k_exp = k_exp;
   p.v_exp = v_exp;
-  p.kv_lens = kv_lens;
-  p.block_table = pg.block_table;
-  p.B = B;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.Lq = Lq;
-  p.Lk = Lk_max;
-  p.group = Hq / Hkv;
-  p.scale_log2 = (float)((double)scale * 1.4426950408889634074);
-  p.num_ctas = pl.num_ctas;
-  p.tile_rows = pl.tile_rows;
-  p.row_tiles = pl.row_tiles;
-  p.page_size = pg.page_size;
-  p.page_shift = pg.block_table ? log2_of(pg.page_size) : 0;
-  p.pages_per_seq = pg.pages_per_seq;
-  p.num_pages = pg.num_pages;
   p.err = error_word_for_current_device();
   if (!p.err) return ATTN_ERR_CUDA;
 
@@ -1423,24 +1474,24 @@ attn_status_t decode_q8_impl(const void* q, const void* k_codes, const void* v_c
   const uint64_t dims[3] = {(uint64_t)d, rows, planes};
   const bool wide = pl.tile_rows == kBlockM;
   const int page_rows = pg.block_table ? pg.page_size : 1 << 16;
-  const int box = wide ? std::min(page_rows, 64) : attn::decode_q8_box_rows(page_rows);
+  const int box = wide ? std::min(page_rows, 64) : attn::decode_rows_box(d, true, page_rows);
   if (!encode_codes(&tk, k_codes, dims, box) || !encode_codes(&tv, v_codes, dims, box))
     return ATTN_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (wide) {
     CUtensorMap tq;
-    const uint64_t dq[2] = {(uint64_t)d, (uint64_t)nrows};
+    const uint64_t dq[2] = {(uint64_t)d, (uint64_t)B * Hq * Lq};
     if (!encode_bf16(&tq, q, 2, dq)) return ATTN_ERR_CUDA;
     e = d == 64 ? attn::launch_decode_q8_wide<64>(tq, tk, tv, p, st)
                 : attn::launch_decode_q8_wide<128>(tq, tk, tv, p, st);
   } else {
-    e = d == 64 ? attn::launch_decode_q8<64>(tk, tv, p, st)
-                : attn::launch_decode_q8<128>(tk, tv, p, st);
+    e = d == 64 ? attn::launch_decode_rows<64, true>(tk, tv, p, st)
+                : attn::launch_decode_rows<128, true>(tk, tv, p, st);
   }
   if (e != cudaSuccess) return ATTN_ERR_CUDA;
-  e = d == 64 ? attn::launch_decode_q8_combine<64>(p, st)
-              : attn::launch_decode_q8_combine<128>(p, st);
+  e = d == 64 ? attn::launch_decode_merge<64>(p, st)
+              : attn::launch_decode_merge<128>(p, st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -1492,8 +1543,8 @@ attn_status_t attn_cache_read_paged_q8(const void* k_pages, const void* v_pages,
 }
 
 size_t attn_decode_q8_workspace_size(int Hq, int Hkv, int Lq, int d, int num_ctas) {
-  Q8Plan pl;
-  return plan_q8(Hq, Hkv, Lq, d, num_ctas, &pl) ? pl.bytes : 0;
+  SharePlan pl;
+  return plan_share(Hq, Hkv, Lq, d, num_ctas, &pl) ? pl.bytes : 0;
 }
 
 attn_status_t attn_decode_splitkv_q8(const void* q, const void* k_cache, const void* v_cache,

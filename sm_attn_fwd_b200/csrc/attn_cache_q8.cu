@@ -15,7 +15,7 @@
 
 #include "attn_params.h"
 #include "cache_q8.cuh"
-#include "cache_q8_params.h"
+#include "decode_params.h"
 #include "ptx.cuh"
 
 namespace attn {

@@ -1,8 +1,8 @@
 // Decode over an 8-bit cache for many query rows per KV head (group * Lq up to 128
-// per tile), for sm_100a: the tensor-memory counterpart of attn_decode_q8.cu.
+// per tile), for sm_100a: the tensor-memory counterpart of attn_decode_rows.cu.
 //
 // With 8 query rows a key's codes are used 8 times and the register path of
-// attn_decode_q8.cu keeps up with memory; with 128 rows (16 drafted tokens x 8
+// attn_decode_rows.cu keeps up with memory; with 128 rows (16 drafted tokens x 8
 // heads) the products are 16 times larger and belong on tcgen05.  Its operands
 // must lie in shared or tensor memory as 16-bit values, so here the codes are
 // expanded: a warpgroup of its own turns each K and V tile, as TMA left it, into the
@@ -22,7 +22,7 @@
 // keys past the end, whatever their codes hold (the construction yields no NaN).
 //
 // Roles (640 threads, one CTA per SM, looping over the pieces of its share of the
-// work, q8_sched.cuh): warp 0 loads the codes, in half tiles of 64 keys; warps 1 and 2
+// work, decode_sched.cuh): warp 0 loads the codes, in half tiles of 64 keys; warps 1 and 2
 // issue the MMAs of even and odd key tiles (warp 1 also loads Q); warp 3 turns scale
 // bytes into factors, a tile ahead (loading them where they are used stalled the
 // expansion 800 cycles per tile); warpgroups 1 and 2 are the softmaxes, each with an S
@@ -42,10 +42,10 @@
 #include <cstdint>
 
 #include "attn_params.h"
-#include "cache_q8_params.h"
+#include "decode_params.h"
 #include "host_once.h"
 #include "ptx.cuh"
-#include "q8_sched.cuh"
+#include "decode_sched.cuh"
 #include "softmax_row.cuh"
 
 namespace attn {
@@ -118,7 +118,7 @@ __device__ __forceinline__ float exp2_pack64(const float (&s)[128], int base, fl
 struct Misc {
   uint32_t tmem_base;
   int abort;
-  q8::Share share;
+  sched::Share share;
   float2 ref[kRefSlots];  // per tile: 2^(kref - 127), vref - 127
 };
 static_assert(sizeof(Misc) == 32 + kRefSlots * 8, "kOffBar");
@@ -146,7 +146,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_decode_q8_wide_kernel(const __grid_constant__ CUtensorMap tm_q,
                                const __grid_constant__ CUtensorMap tm_k,
-                               const __grid_constant__ CUtensorMap tm_v, const DecodeQ8Params p) {
+                               const __grid_constant__ CUtensorMap tm_v, const DecodeParams p) {
   using C = WCfg<D>;
   constexpr int S = C::kStages;
   constexpr int R = C::kRaw;
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == 0) {
-    const q8::Share sh = q8::find_share(p.kv_lens, p.B, p.Lk, units, blockIdx.x, gridDim.x, err);
+    const sched::Share sh = sched::find_share(p.kv_lens, p.B, p.Lk, units, blockIdx.x, gridDim.x, err);
     if (lane == 0) {
       misc->share = sh;
       misc->abort = 0;
@@ -226,9 +226,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = misc->tmem_base;
-  const q8::Share& share = misc->share;
+  const sched::Share& share = misc->share;
   const int total = share.tiles;
-  //q8::let_next_kernel_launch();
+  //sched::let_next_kernel_launch();
   bool ok = true;
 
   if (warp < 4) {
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_box = 64 / rows;  // at most 4
       const uint64_t policy = ptx::l2_policy_evict_first();
       int hj = 0, n_k = 0;  // half tiles issued: V's hj, K's n_k
-      q8::Walk w;
+      sched::Walk w;
       for (w.start(share, p.kv_lens, p.Lk); w.valid() && ok; w.next(p.kv_lens, p.Lk, units)) {
         const int hkv = w.h / p.row_tiles;
         const int key_end = min(w.t1 * 128, w.len);
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // tile ahead of their use, the page ids two.
       const int rows = paged && p.page_size < 128 ? p.page_size : 128;
       const int row_shift = 31 - __clz(rows);
-      q8::Walk a;  // of the tile whose page ids load next
+      sched::Walk a;  // of the tile whose page ids load next
       a.start(share, p.kv_lens, p.Lk);
       int at = a.t0;
       struct Tile {
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int base = 0;   // tiles of the earlier pieces
       int n = 0;      // own tiles done
       int piece = 0;
-      q8::Walk w;
+      sched::Walk w;
       for (w.start(share, p.kv_lens, p.Lk); w.valid() && ok;
            w.next(p.kv_lens, p.Lk, units), ++piece) {
         const int end = base + w.t1 - w.t0;
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // barrier parities, in one register: own tiles done (bit 0), odd tiles of the earlier
     // pieces (bit 1), pieces done (bit 2); bit 3: a piece is done
     uint32_t ph = 0;
-    q8::Walk w;
+    sched::Walk w;
     for (w.start(share, p.kv_lens, p.Lk); w.valid() && ok;
          w.next(p.kv_lens, p.Lk, units), ph = (ph ^ 4u) | 8u) {
       const int end = base + w.t1 - w.t0;
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D>
 cudaError_t launch_decode_q8_wide(const CUtensorMap& tq, const CUtensorMap& tk,
-                                  const CUtensorMap& tv, const DecodeQ8Params& p,
+                                  const CUtensorMap& tv, const DecodeParams& p,
                                   cudaStream_t stream) {
   auto kern = attn_decode_q8_wide_kernel<D>;
   constexpr int smem = WCfg<D>::kSmemAlloc;
@@ -699,10 +699,10 @@ cudaError_t launch_decode_q8_wide(const CUtensorMap& tq, const CUtensorMap& tk,
 }
 
 template cudaError_t launch_decode_q8_wide<64>(const CUtensorMap&, const CUtensorMap&,
-                                               const CUtensorMap&, const DecodeQ8Params&,
+                                               const CUtensorMap&, const DecodeParams&,
                                                cudaStream_t);
 template cudaError_t launch_decode_q8_wide<128>(const CUtensorMap&, const CUtensorMap&,
-                                                const CUtensorMap&, const DecodeQ8Params&,
+                                                const CUtensorMap&, const DecodeParams&,
                                                 cudaStream_t);
 
 }  // namespace attn

@@ -28,6 +28,7 @@
 
 #include "attn_params.h"
 #include "attn_prefix_params.h"
+#include "decode_sched.cuh"
 #include "host_once.h"
 #include "ptx.cuh"
 #include "softmax_row.cuh"
@@ -167,6 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = misc->tmem_base;
+  // the decode of the sequences' own caches needs nothing from here: it may start as
+  // soon as an SM is free
+  sched::let_next_kernel_launch();
 
   if (warp < 4) {
     ptx::regs_dec<kRegsLow>();

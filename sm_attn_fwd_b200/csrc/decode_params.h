@@ -1,4 +1,5 @@
-// Launch parameters of the 8-bit cache kernels, shared by host and device.
+// Launch parameters of the 8-bit cache's kernels and of the decodes that share out their
+// work (decode_sched.cuh), used by host and device.
 #pragma once
 
 #include <cstdint>
@@ -25,14 +26,21 @@ struct CacheParams {
   int pages_per_seq, num_pages;
 };
 
-// Decode over an 8-bit cache.  The work is shared among num_ctas CTAs as q8_sched.cuh
+// Decode over an 8-bit cache, or a bf16 one with few query rows.  The work is shared among num_ctas CTAs as decode_sched.cuh
 // describes; CTA c's partial results are slots 2 c and 2 c + 1 of the workspace.
-struct DecodeQ8Params {
+struct DecodeParams {
   const void* q;  // bf16 [B, Hq, Lq, d]
   void* o;        // bf16 [B, Hq, Lq, d]
   float* lse;     // fp32 [B, Hq, Lq]
   float* ws_o;    // fp32 [2 num_ctas, tile_rows, d]
   float* ws_lse;  // fp32 [2 num_ctas, tile_rows]
+  // behind a shared prefix: its splits' partial results, and where the units that one
+  // CTA computes go instead of o and lse (null otherwise)
+  const float* prefix_o;    // fp32 [num_prefix, B*Hq*Lq, d]
+  const float* prefix_lse;  // fp32 [num_prefix, B*Hq*Lq]
+  float* own_o;             // fp32 [B*Hq*Lq, d]
+  float* own_lse;           // fp32 [B*Hq*Lq]
+  int num_prefix;
   const uint8_t* k_exp;
   const uint8_t* v_exp;
   const int32_t* kv_lens;
@@ -46,13 +54,15 @@ struct DecodeQ8Params {
   int page_size, page_shift, pages_per_seq, num_pages;
 };
 
-// Cost, in key tiles, of starting on and finishing a unit (q8_sched.cuh).
-constexpr int kQ8Piece = 3;
+// Cost, in key tiles, of starting on and finishing a unit (decode_sched.cuh).
+constexpr int kPieceTiles = 3;
 
-// Query rows per unit for `rows` query rows per KV head.  Up to 16 (32 at d = 64)
-// go through mma.m16n8k16 (attn_decode_q8.cu), the smallest of its tiles that holds
-// them; more are worth expanding the codes for tcgen05 (attn_decode_q8_wide.cu).
-inline int decode_q8_tile_rows(int d, long long rows) {
+// Query rows per unit for `rows` query rows per KV head.  Up to 16 (32 at d = 64) go
+// through mma.m16n8k16 (attn_decode_rows.cu), the smallest of its tiles that holds them;
+// for more, tcgen05 tiles of 128 rows are faster.  16 sequences x 8 KV heads x 16384
+// keys in 8 bits, 32 rows: 213 us through tcgen05 against 250 at d = 128, 179 against
+// 130 at d = 64; 16 rows: 110 and 80 us through m16n8k16.
+inline int decode_tile_rows(int d, long long rows) {
   if (rows <= 8) return 8;
   if (rows <= 16) return 16;
   return d == 64 && rows <= 32 ? 32 : 128;

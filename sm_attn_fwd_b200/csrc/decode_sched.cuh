@@ -1,15 +1,15 @@
 // How the 8-bit decode kernels share a batch of ragged sequences among their CTAs.
 //
 // A unit is one (sequence, KV head, tile of query rows); it has as many key tiles
-// (128 keys) as its sequence.  A unit with n > 0 tiles costs n + kPiece: starting on
-// and finishing a unit takes about as long as kPiece tiles (with 28 one-tile units in
+// (128 keys) as its sequence.  A unit with n > 0 tiles costs n + kPieceTiles: starting on
+// and finishing a unit takes about as long as kPieceTiles tiles (with 28 one-tile units in
 // one CTA and 28 tiles of two units in another, a batch of ragged lengths from 1 to
 // 4099 took 49 us where one of equal lengths and more tiles took 30).  All units, in
 // the order (sequence, head, row tile), form one line of length T, and CTA c of G
 // takes [c T / G, (c + 1) T / G) of it (G = the number of CTAs, at most T; the rest get
 // nothing): equal work whatever the lengths, one start-up per CTA, and a unit is cut
 // only where a CTA's share ends, its pieces in neighbouring CTAs.  Tile t of a unit
-// that starts at `base` lies at base + kPiece + t.  The lengths are known on the device
+// that starts at `base` lies at base + kPieceTiles + t.  The lengths are known on the device
 // only, so every CTA (and the combine) works its part out from kv_lens.
 //
 // A unit that one CTA computes whole is written to the outputs by it.  A CTA has at
@@ -24,17 +24,17 @@
 #include <cuda_runtime.h>
 
 #include "attn_params.h"
-#include "cache_q8_params.h"
+#include "decode_params.h"
 
 namespace attn {
-namespace q8 {
+namespace sched {
 
 // A sequence's length in [0, Lk], its key tiles, and the cost of a unit of it.
 __device__ __forceinline__ int seq_len(const int32_t* kv_lens, int b, int Lk) {
   return min(max(__ldg(kv_lens + b), 0), Lk);
 }
 __device__ __forceinline__ int tiles_of(int len) { return (int)(((unsigned)len + 127u) >> 7); }
-__device__ __forceinline__ int cost_of(int len) { return len > 0 ? tiles_of(len) + kQ8Piece : 0; }
+__device__ __forceinline__ int cost_of(int len) { return len > 0 ? tiles_of(len) + kPieceTiles : 0; }
 
 // [first(c), first(c + 1)) is CTA c's part of a line of length T over G <= T CTAs, the
 // first T % G of them one longer; of(x) is the CTA that holds x.
@@ -71,13 +71,13 @@ struct Walk {
     if (s.g0 >= s.g1) return;
     len = seq_len(kv_lens, b, Lk);
     tiles = tiles_of(len);
-    t0 = max(0, s.g0 - base - kQ8Piece);
-    t1 = min(tiles, max(0, g1 - base - kQ8Piece));
+    t0 = max(0, s.g0 - base - kPieceTiles);
+    t1 = min(tiles, max(0, g1 - base - kPieceTiles));
   }
   // false after the last piece (and for a share that ends before a unit's first tile)
   __device__ __forceinline__ bool valid() const { return t0 < t1; }
   __device__ __forceinline__ void next(const int32_t* kv_lens, int Lk, int units) {
-    base += tiles + kQ8Piece;
+    base += tiles + kPieceTiles;
     t0 = t1 = 0;
     if (base >= g1) return;
     if (++h == units) {
@@ -87,7 +87,7 @@ struct Walk {
       } while (len == 0);
       tiles = tiles_of(len);
     }
-    t1 = min(tiles, max(0, g1 - base - kQ8Piece));
+    t1 = min(tiles, max(0, g1 - base - kPieceTiles));
   }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
   __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (t0 > 0 ? 0 : 1); }
@@ -144,5 +144,5 @@ __device__ __forceinline__ void let_next_kernel_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-}  // namespace q8
+}  // namespace sched
 }  // namespace attn

@@ -71,14 +71,22 @@ def test_split_plan_covers_the_prefix():
 
 
 def test_workspace_holds_both_parts():
-    B, Hq, Hkv, Lq, Lp, Lk, d = 4, 16, 2, 2, 3000, 700, 64
-    np_, _ = plan(B, Hq, Hkv, Lq, Lp, 5)
-    ns, _ = ab.attn_decode_num_splits(B, Hq, Hkv, Lq, Lk, d)
-    rows = B * Hq * Lq
-    want = ((np_ + ns) * rows * d * 4 + 255) // 256 * 256 + (np_ + ns) * rows * 4
-    assert ab.attn_decode_shared_prefix_workspace_size(B, Hq, Hkv, Lq, Lp, Lk, d, 5) == want
+    """Few query rows per KV head: the prefix's splits, a row per output row and two
+    partials per CTA; many: the prefix's splits and the decode's."""
+    B, Hkv, Lp, Lk = 4, 2, 3000, 700
+    for d, Hq, Lq, tile in ((64, 16, 2, 16), (128, 16, 1, 8), (64, 16, 4, 32), (128, 16, 4, 0),
+                            (64, 32, 4, 0)):
+        np_, _ = plan(B, Hq, Hkv, Lq, Lp, 5)
+        ns, _ = ab.attn_decode_num_splits(B, Hq, Hkv, Lq, Lk, d)
+        rows = B * Hq * Lq
+        sms = 148  # without a device
+        if ab.torch.cuda.is_available():
+            sms = ab.torch.cuda.get_device_properties(0).multi_processor_count
+        part = (np_ + 1) * rows + 2 * sms * tile if tile else (np_ + ns) * rows
+        want = (part * d * 4 + 255) // 256 * 256 + part * 4
+        assert ab.attn_decode_shared_prefix_workspace_size(B, Hq, Hkv, Lq, Lp, Lk, d, 5) == want
     with pytest.raises(ab.AttnError):
-        ab.attn_decode_shared_prefix_workspace_size(B, Hq, 3, Lq, Lp, Lk, d)
+        ab.attn_decode_shared_prefix_workspace_size(B, 16, 3, 1, Lp, Lk, 64)
 
 
 def test_binding_rejects_host_tensors():
