@@ -24,8 +24,8 @@
 // Roles (640 threads, one CTA per SM, looping over the pieces of its share of the
 // work, decode_sched.cuh): warp 0 loads the codes, in half tiles of 64 keys; warps 1 and 2
 // issue the MMAs of even and odd key tiles (warp 1 also loads Q); warp 3 turns scale
-// bytes into factors, a tile ahead (loading them where they are used stalled the
-// expansion 800 cycles per tile); warpgroups 1 and 2 are the softmaxes, each with an S
+// bytes into factors (loading them where they are used stalled the expansion 800
+// cycles per tile); warpgroups 1 and 2 are the softmaxes, each with an S
 // and an O of its own in tensor memory; warpgroup 3 expands K tiles and warpgroup 4
 // V tiles (one warpgroup for both took 2700 cycles per tile).  At the end of a piece
 // warpgroup 1 merges the two O and writes the result, while the loads, the expansion
@@ -53,10 +53,12 @@ namespace {
 
 constexpr int kThreads = 640;
 // registers per thread of the warpgroups: loads and MMAs; softmax (two); expansion of K
-// and of V.  48 + 2 * 168 + 2 * 48 = 5 * 96, the launch's.
+// and of V.  48 + 2 * 176 + 2 * 40 = 5 * 96, the launch's.
 constexpr int kRegsIssue = 48;
-constexpr int kRegsExpand = 48;
-constexpr int kRegsSoftmax = 168;
+constexpr int kRegsExpand = 40;
+constexpr int kRegsSoftmax = 176;
+// more than the launch's registers would wait for ever
+static_assert(kRegsIssue + 2 * kRegsSoftmax + 2 * kRegsExpand <= 5 * 96, "register shares");
 constexpr int kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -289,82 +291,94 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 3) {
       // -------------------------------------------------------- scale factors
-      // Lane l takes keys l, 32 + l, 64 + l and 96 + l of a tile.  The bytes load one
-      // tile ahead of their use, the page ids two.
-      const int rows = paged && p.page_size < 128 ? p.page_size : 128;
-      const int row_shift = 31 - __clz(rows);
+      // Lane l takes keys 4 l .. 4 l + 3 of a tile: one 32-bit word of scale bytes for K
+      // and one for V, loaded kAhead tiles ahead of their use (page ids one more), as a
+      // load from memory can take longer than a tile (3 ahead: no faster, 5 % slower in
+      // one measurement).
+      constexpr int kAhead = 2;
       sched::Walk a;  // of the tile whose page ids load next
       a.start(share, p.kv_lens, p.Lk);
       int at = a.t0;
       struct Tile {
-        int k0, end, bh, z;  // z: pool index of this lane's page slice
+        int key, n, z;  // the lane's first key, its live keys (0..4), and its pool index
       };
       auto fetch = [&]() -> Tile {  // the tile at `a`, which moves on
-        Tile f = {0, 0, 0, -1};
+        Tile f = {0, 0, 0};
         if (!a.valid()) return f;
         const int hkv = a.h / p.row_tiles;
-        f.k0 = at * 128;
-        f.end = min(a.t1 * 128, a.len);
-        f.bh = a.b * p.Hkv + hkv;
-        const int key = f.k0 + lane * rows;
-        if (paged && lane < 128 / rows && key < f.end) f.z = pool(a.b, hkv, key);
+        f.key = at * 128 + 4 * lane;
+        f.n = max(0, min(4, min(a.t1 * 128, a.len) - f.key));
+        f.z = a.b * p.Hkv + hkv;
+        if (paged && f.n > 0) f.z = pool(a.b, hkv, f.key);
         if (++at == a.t1) {
           a.next(p.kv_lens, p.Lk, units);
           at = a.t0;
         }
         return f;
       };
-      // scale bytes of a tile (0 past the end)
-      auto load_exps = [&](const Tile& f, uint32_t (&k)[4], uint32_t (&v)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = f.k0 + i * 32 + lane;
-          const int zi = __shfl_sync(0xffffffffu, f.z, paged ? (i * 32 + lane) >> row_shift : 0);
-          const bool live = key < f.end && (!paged || zi >= 0);
-          const long long row = paged ? ((long long)zi << p.page_shift) + (key & (p.page_size - 1))
-                                      : (long long)f.bh * p.Lk + key;
-          k[i] = live ? __ldg(p.k_exp + row) : 0u;
-          v[i] = live ? __ldg(p.v_exp + row) : 0u;
-        }
+      // The scale bytes of a tile's keys, 0 past the end.  Words where they are aligned
+      // and inside the row of the cache, else single bytes.
+      auto load_word = [&](const uint8_t* exps, const Tile& f) -> uint32_t {
+        if (f.n == 0 || f.z < 0) return 0u;
+        const uint8_t* src =
+            exps + (paged ? ((long long)f.z << p.page_shift) + (f.key & (p.page_size - 1))
+                          : (long long)f.z * p.Lk + f.key);
+        const bool inside = paged || f.key + 3 < p.Lk;
+        if (inside && (reinterpret_cast<uintptr_t>(src) & 3) == 0)
+          return __ldg(reinterpret_cast<const uint32_t*>(src));
+        uint32_t w = 0;
+        for (int i = 0; i < f.n; ++i) w |= (uint32_t)__ldg(src + i) << (8 * i);
+        return w;
       };
-      // bf16 exponent of 2^(120 + e - ref); 0 (a factor of zero) for e = 0 (past the
+      auto byte_max = [](uint32_t w) -> int {
+        w = __vmaxu4(w, w >> 16);
+        return (int)__reduce_max_sync(0xffffffffu, __vmaxu4(w, w >> 8) & 0xffu);
+      };
+      // bf16 exponents of 2^(120 + e - ref); 0 (a factor of zero) for e = 0 (past the
       // end) and underflow.  At most 254: ref >= e - 7.
-      auto factor = [](int e, int ref) -> uint8_t {
-        return e > 0 ? (uint8_t)max(247 + e - ref, 0) : (uint8_t)0;
+      auto factors = [](uint32_t w, int ref) -> uint32_t {
+        uint32_t r = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = (int)(w >> (8 * i) & 0xffu);
+          if (e > 0) r |= (uint32_t)max(247 + e - ref, 0) << (8 * i);
+        }
+        return r;
       };
-      uint32_t k[4], v[4];
-      load_exps(fetch(), k, v);
+      uint32_t k[kAhead], v[kAhead], live[kAhead];  // live: mask of the live keys' bytes
+      auto load = [&](const Tile& f, int i) {
+        k[i] = load_word(p.k_exp, f);
+        v[i] = load_word(p.v_exp, f);
+        live[i] = f.n == 4 ? ~0u : (1u << (8 * f.n)) - 1u;
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) load(fetch(), i);
       Tile f = fetch();
-      for (int j = 0; j < total; ++j) {
-        uint32_t kn[4], vn[4];
-        load_exps(f, kn, vn);
-        f = fetch();
-        const int kref = (int)__reduce_max_sync(0xffffffffu, max(max(k[0], k[1]), max(k[2], k[3])));
-        // vref is bounded so that P' = p 2^(vref - 127) stays clear of both ends of fp32
-        const int vref = min(
-            max((int)__reduce_max_sync(0xffffffffu, max(max(v[0], v[1]), max(v[2], v[3]))), 67),
-            240);
-        const int fs = j % kFactorSlots;
-        ok = ptx::mbar_wait_a(BAR(kFactorEmpty + fs), ((uint32_t)(j / kFactorSlots) & 1u) ^ 1u,
-                              abort_flag, err, kDevErrTimeoutProducer);
-        ok = __all_sync(0xffffffffu, ok);
+      for (int j = 0; j < total;) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i, ++j) {
+          if (j >= total) break;
+          const uint32_t kw = k[i] & live[i], vw = v[i] & live[i];
+          load(f, i);
+          f = fetch();
+          const int kref = byte_max(kw);
+          // vref is bounded so that P' = p 2^(vref - 127) stays clear of both ends of fp32
+          const int vref = min(max(byte_max(vw), 67), 240);
+          const int fs = j % kFactorSlots;
+          ok = ptx::mbar_wait_a(BAR(kFactorEmpty + fs), ((uint32_t)(j / kFactorSlots) & 1u) ^ 1u,
+                                abort_flag, err, kDevErrTimeoutProducer);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          uint32_t* out = reinterpret_cast<uint32_t*>(smem + C::kOffFactor + fs * 256);
+          out[lane] = factors(kw, kref);
+          out[32 + lane] = factors(vw, vref);
+          if (lane == 0)
+            misc->ref[j % kRefSlots] =
+                make_float2(__uint_as_float((uint32_t)max(kref, 1) << 23), (float)(vref - 127));
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_a(BAR(kFactorFull + fs));
+        }
         if (!ok) break;
-        uint8_t* out = smem + C::kOffFactor + fs * 256;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          out[i * 32 + lane] = factor((int)k[i], kref);
-          out[128 + i * 32 + lane] = factor((int)v[i], vref);
-        }
-        if (lane == 0)
-          misc->ref[j % kRefSlots] =
-              make_float2(__uint_as_float((uint32_t)max(kref, 1) << 23), (float)(vref - 127));
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_a(BAR(kFactorFull + fs));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          k[i] = kn[i];
-          v[i] = vn[i];
-        }
       }
     } else {
       // ------------------------------- MMA issuer of the tiles of parity x
