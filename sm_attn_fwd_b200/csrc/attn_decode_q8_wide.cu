@@ -121,6 +121,7 @@ struct Misc {
   uint32_t tmem_base;
   int abort;
   sched::Share share;
+  int total;
   float2 ref[kRefSlots];  // per tile: 2^(kref - 127), vref - 127
 };
 static_assert(sizeof(Misc) == 32 + kRefSlots * 8, "kOffBar");
@@ -186,8 +187,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     const sched::Share sh = sched::find_share(p.kv_lens, p.B, p.Lk, units, blockIdx.x, gridDim.x, err);
+    const int n = sched::count_tiles(sh, p.kv_lens, p.Lk, units);
     if (lane == 0) {
       misc->share = sh;
+      misc->total = n;
       misc->abort = 0;
     }
   } else if (warp == 1) {
@@ -229,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = misc->tmem_base;
   const sched::Share& share = misc->share;
-  const int total = share.tiles;
+  const int total = misc->total;  // key tiles of this CTA
   //sched::let_next_kernel_launch();
   bool ok = true;
 

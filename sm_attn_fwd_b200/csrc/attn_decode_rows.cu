@@ -761,6 +761,7 @@ __global__ void __launch_bounds__(256) attn_decode_merge_kernel(const DecodePara
   const int rr = r % p.tile_rows;
   // the line's length, and what lies before sequence b
   int all = 0, before = 0;
+#pragma unroll 4
   for (int i = lane; i < p.B; i += 32) {
     const int n = sched::cost_of(sched::seq_len(p.kv_lens, i, p.Lk));
     all += n;

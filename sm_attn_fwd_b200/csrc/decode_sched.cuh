@@ -53,7 +53,6 @@ __device__ __forceinline__ int ctas_used(int T, int ctas) { return min(T, ctas);
 struct Share {
   int g0, g1, base;
   int b, h;
-  int tiles;  // key tiles in the share
 };
 
 // Walks the pieces of a share: tiles [t0, t1) of the `tiles` of unit (b, h).
@@ -99,6 +98,7 @@ __device__ __forceinline__ Share find_share(const int32_t* kv_lens, int B, int L
   const int lane = threadIdx.x & 31;
   bool bad = false;
   int sum = 0;
+#pragma unroll 4  // the loads of four rounds in flight together
   for (int b = lane; b < B; b += 32) {
     const int len = __ldg(kv_lens + b);
     if (len < 0 || len > Lk) bad = true;
@@ -106,7 +106,7 @@ __device__ __forceinline__ Share find_share(const int32_t* kv_lens, int B, int L
   }
   if (bad && cta == 0) atomicOr(err, kDevErrBadKvLen);
   const int T = __reduce_add_sync(0xffffffffu, sum) * units;
-  Share s = {0, 0, 0, 0, 0, 0};
+  Share s = {0, 0, 0, 0, 0};
   const int G = ctas_used(T, ctas);
   if (cta >= G) return s;
   const Split split(T, G);
@@ -133,9 +133,16 @@ __device__ __forceinline__ Share find_share(const int32_t* kv_lens, int B, int L
     }
     s.base += __shfl_sync(0xffffffffu, upto, 31);
   }
-  Walk w;
-  for (w.start(s, kv_lens, Lk); w.valid(); w.next(kv_lens, Lk, units)) s.tiles += w.t1 - w.t0;
   return s;
+}
+
+// The key tiles of a share.
+__device__ __forceinline__ int count_tiles(const Share& s, const int32_t* kv_lens, int Lk,
+                                           int units) {
+  int n = 0;
+  Walk w;
+  for (w.start(s, kv_lens, Lk); w.valid(); w.next(kv_lens, Lk, units)) n += w.t1 - w.t0;
+  return n;
 }
 
 // Lets the kernel that follows in the stream start launching (it waits for this one's
