@@ -1,12 +1,11 @@
 // Writing an 8-bit KV cache and reading it back (format in cache_q8.cuh).
 //
 // Both kernels are one pass over the rows and bound by memory: append reads
-// 2 d bytes and writes d + 1 per row, read-back the reverse.  A row belongs to
-// d / 8 neighbouring lanes (append: 8 bf16 values, one 16-byte load each) or
-// d / 16 (read-back: 16 codes, one 16-byte load each), so a warp's accesses cover
-// whole consecutive rows; the row maximum is a few shuffles inside the lane
-// group.  Each lane group handles its K row and its V row together, two loads in
-// flight per thread.
+// 2 d bytes and writes d + 1 per row, read-back the reverse.  A row belongs to d / 8
+// neighbouring lanes, eight values each: 16 bytes of bf16, 8 of codes, so a warp's
+// loads and stores cover whole consecutive rows (read-back with 16 codes per lane
+// stored half sectors: 5.1 TB/s instead of 6.7).  The row maximum is a few shuffles
+// inside the lane group.  Each lane group handles its K row and its V row together.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -134,18 +133,18 @@ __global__ void __launch_bounds__(kCacheThreads) attn_cache_append_kernel(const 
   }
 }
 
-// 16 codes times 2^(e - 127) -> 16 bf16 values (32 bytes).  Two codes sign-extended
-// into 16-bit halves, shifted by 4 and masked, read as bf16, are the values times
-// 2^-120; one packed multiply finishes two of them, exactly except below bf16's normal
-// range, where it rounds to nearest even.
-__device__ __forceinline__ void restore16(const uint4& c, int e, uint4 (&out)[2]) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  uint32_t r[8];
+// Eight codes times 2^(e - 127) -> eight bf16 values (16 bytes).  Two codes
+// sign-extended into 16-bit halves, shifted by 4 and masked, read as bf16, are the
+// values times 2^-120; one packed multiply finishes two of them, exactly except below
+// bf16's normal range, where it rounds to nearest even.
+__device__ __forceinline__ uint4 restore8(const uint2& c, int e) {
+  const uint32_t w[2] = {c.x, c.y};
+  uint32_t r[4];
   // 2^(e - 7); above bf16's range (e > 134) 2^120 and 2^(e - 127) one after the other
   const uint32_t x = e <= 134 ? (uint32_t)(e + 120) : 247u;
   const uint32_t f = x << 7 | x << 23;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     uint32_t v;
     asm("prmt.b32 %0, %1, 0, %2;" : "=r"(v) : "r"(w[i >> 1]), "r"(i & 1 ? 0xb3a2 : 0x9180));
     v = (v << 4) & 0x87f087f0u;
@@ -156,28 +155,25 @@ __device__ __forceinline__ void restore16(const uint4& c, int e, uint4 (&out)[2]
   if (e > 134) {
     const uint32_t f2 = (uint32_t)e << 7 | (uint32_t)e << 23;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r[i]),
                                        *reinterpret_cast<const __nv_bfloat162*>(&f2));
       r[i] = *reinterpret_cast<const uint32_t*>(&y);
     }
   }
   // NaN codes (magnitude 0x7f) come back as NaN: a carry out of a byte marks them
-  const uint32_t nan = (((w[0] & 0x7f7f7f7fu) + 0x01010101u) | ((w[1] & 0x7f7f7f7fu) + 0x01010101u) |
-                        ((w[2] & 0x7f7f7f7fu) + 0x01010101u) | ((w[3] & 0x7f7f7f7fu) + 0x01010101u)) &
-                       0x80808080u;
-  if (nan) {
+  if ((((w[0] & 0x7f7f7f7fu) + 0x01010101u) | ((w[1] & 0x7f7f7f7fu) + 0x01010101u)) &
+      0x80808080u) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 8; ++i)
       if (((w[i >> 2] >> (8 * (i & 3))) & 0x7fu) == 0x7fu) r[i >> 1] |= 0x7fffu << (16 * (i & 1));
   }
-  out[0] = make_uint4(r[0], r[1], r[2], r[3]);
-  out[1] = make_uint4(r[4], r[5], r[6], r[7]);
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 template <int D, int U>
 __global__ void __launch_bounds__(kCacheThreads) attn_cache_read_kernel(const CacheParams p) {
-  constexpr int kLanes = D / 16;
+  constexpr int kLanes = D / 8;
   constexpr int kGroups = kCacheThreads / kLanes;
   const int part = threadIdx.x % kLanes;
   const int bh = blockIdx.z * gridDim.y + blockIdx.y;
@@ -189,35 +185,29 @@ __global__ void __launch_bounds__(kCacheThreads) attn_cache_read_kernel(const Ca
     if (first == 0 && h == 0 && part == 0) atomicOr(p.err, kDevErrBadKvLen);
     return;
   }
-  uint4 kc[U], vc[U];
+  uint2 kc[U], vc[U];
   int ke[U], ve[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int j = first + u * kGroups;
-    kc[u] = vc[u] = make_uint4(0, 0, 0, 0);
+    kc[u] = vc[u] = make_uint2(0, 0);
     ke[u] = ve[u] = 1;
     if (j >= len) continue;
     const long long src = cache_row(p, b, h, j);
     if (src < 0) continue;  // reads as zeros
-    kc[u] = __ldcs(reinterpret_cast<const uint4*>(p.k_codes) + src * kLanes + part);
-    vc[u] = __ldcs(reinterpret_cast<const uint4*>(p.v_codes) + src * kLanes + part);
+    kc[u] = __ldcs(reinterpret_cast<const uint2*>(p.k_codes) + src * kLanes + part);
+    vc[u] = __ldcs(reinterpret_cast<const uint2*>(p.v_codes) + src * kLanes + part);
     ke[u] = __ldg(p.k_exp + src);
     ve[u] = __ldg(p.v_exp + src);
   }
-  const long long out0 = ((long long)bh * p.Lk * kLanes + part) * 2;
+  const long long out0 = (long long)bh * p.Lk * kLanes + part;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int j = first + u * kGroups;
     if (j >= len) continue;
-    uint4 ko[2], vo[2];
-    restore16(kc[u], ke[u], ko);
-    restore16(vc[u], ve[u], vo);
-    const long long dst = out0 + (long long)j * (kLanes * 2);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      __stcs(reinterpret_cast<uint4*>(p.k_out) + dst + i, ko[i]);
-      __stcs(reinterpret_cast<uint4*>(p.v_out) + dst + i, vo[i]);
-    }
+    const long long dst = out0 + (long long)j * kLanes;
+    __stcs(reinterpret_cast<uint4*>(p.k_out) + dst, restore8(kc[u], ke[u]));
+    __stcs(reinterpret_cast<uint4*>(p.v_out) + dst, restore8(vc[u], ve[u]));
   }
 }
 
@@ -251,7 +241,7 @@ cudaError_t launch_cache_append(const CacheParams& p, cudaStream_t stream) {
 
 template <int D>
 cudaError_t launch_cache_read(const CacheParams& p, cudaStream_t stream) {
-  constexpr int kLanes = D / 16, U = kRowsPerGroup;
+  constexpr int kLanes = D / 8, U = kRowsPerGroup;
   const long long pairs = (long long)p.B * p.Hkv;
   if (many_rows(pairs * p.Lk, kLanes))
     attn_cache_read_kernel<D, U>
