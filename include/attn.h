@@ -407,7 +407,7 @@ size_t attn_decode_shared_prefix_workspace_size(int B, int Hq, int Hkv, int Lq, 
  * Arguments
  *   q        [B, Hq, Lq, d] bf16, read;  o [B, Hq, Lq, d] bf16, lse [B, Hq, Lq]
  *            fp32, written
- *   k_prefix, v_prefix  [Hkv, Lp, d] bf16, read;  Lp >= 1
+ *   k_prefix, v_prefix  [Hkv, Lp, d] bf16, read;  1 <= Lp < 2^31 - 2^20
  *   k_cache, v_cache    [B, Hkv, Lk_max, d] bf16, read only below kv_lens[b]
  *   kv_lens  [B] int32 DEVICE array, each in [0, Lk_max] (0: the prefix alone); an
  *            entry outside is clamped and flags the device error word
@@ -479,7 +479,8 @@ attn_status_t attn_decode_shared_prefix_paged(
  *   k_cache, v_cache, k_exp, v_exp  the cache above, written
  *   kv_lens  [B] int32 DEVICE array, each in [n_b, Lk_max]
  *   new_lens [B] int32 DEVICE array, each in [0, Ln], or NULL
- *   B, Hkv, Ln, Lk_max >= 1, B * Hkv * Ln < 2^31; d in {64, 128}
+ *   B, Hkv, Ln, Lk_max >= 1, B * Hkv * Ln < 2^31 - 4096 (else UNSUPPORTED); d in
+ *   {64, 128}
  * A sequence whose kv_lens or new_lens entry is out of range is skipped and
  * flags the device error word (ATTN_ERR_INVALID_ARG).
  * Errors: INVALID_ARG / UNSUPPORTED before any launch; CUDA on launch failure.
@@ -514,7 +515,8 @@ attn_status_t attn_cache_append_paged_q8(const void* k, const void* v, void* k_p
  *   k, v     [B, Hkv, Lk_max, d] bf16, rows below kv_lens[b] written (the exact
  *            values code * 2^(e - 127), which bf16 holds in its normal range); the
  *            other rows are left as they were
- *   B * Hkv * Lk_max < 2^31; the rest as for attn_cache_append_q8
+ *   B * Hkv * Lk_max < 2^31 - 4096 (else UNSUPPORTED); the rest as for
+ *   attn_cache_append_q8
  * Errors: INVALID_ARG / UNSUPPORTED before any launch; CUDA on launch failure.
  */
 attn_status_t attn_cache_read_q8(const void* k_cache, const void* v_cache, const uint8_t* k_exp,

@@ -667,7 +667,11 @@ def _workspace(workspace, size_fn, size_args, q, where):
     """(tensor, bytes) of a workspace, allocated with size_fn(*size_args) bytes when not
     given."""
     if workspace is None:
-        need = size_fn(*size_args)
+        if torch.cuda.current_device() != q.get_device():  # the plan goes by its SM count
+            with torch.cuda.device(q.get_device()):
+                need = size_fn(*size_args)
+        else:
+            need = size_fn(*size_args)
         if need == 0:
             raise AttnError(ATTN_ERR_INVALID_ARG, where)
         return q.new_empty(need, dtype=torch.uint8), need

@@ -1142,6 +1142,8 @@ bool set_share_shape(attn::DecodeParams* p, const void* q, const int32_t* kv_len
 // ------------------------------------------------------- shared prefix
 namespace {
 
+constexpr int kMaxPrefix = 0x7fffffff - (1 << 20);  // key counters are 32-bit
+
 // Splits of the prefix: row tiles (128 rows of one KV head, whatever their
 // sequence) in pairs, and np chunks of whole key tiles.
 struct PrefixPlan {
@@ -1151,6 +1153,7 @@ struct PrefixPlan {
 
 bool plan_prefix(int B, int Hq, int Hkv, int Lq, int Lp, int num_splits, PrefixPlan* pp) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Lq < 1 || Lp < 1 || num_splits < 0 || Hq % Hkv) return false;
+  if (Lp > kMaxPrefix) return false;
   const long long G = (long long)(Hq / Hkv) * Lq;
   if (G > 0x7fffffffLL / 2) return false;
   pp->nb = G <= kBlockM ? (int)std::min<long long>(kBlockM / G, B) : 1;
@@ -1372,6 +1375,9 @@ attn_status_t attn_decode_shared_prefix_paged(
 // ------------------------------------------------------- 8-bit KV cache
 namespace {
 
+// Rows of one call: row counters are 32-bit, with room for the last block's.
+constexpr long long kMaxCacheRows = 0x7fffffffLL - 4096;
+
 // Arguments shared by append and read-back.
 attn_status_t cache_params(const void* k_codes, const void* v_codes, const uint8_t* k_exp,
                            const uint8_t* v_exp, const int32_t* kv_lens, int B, int Hkv, int Lk,
@@ -1407,7 +1413,7 @@ attn_status_t append_impl(const void* k, const void* v, void* k_codes, void* v_c
   if (vs != ATTN_OK) return vs;
   if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return ATTN_ERR_INVALID_ARG;
   if (Ln < 1 || (new_lens && !aligned(new_lens, 4))) return ATTN_ERR_INVALID_ARG;
-  if ((long long)B * Hkv > 0x7fffffffLL / Ln) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)B * Hkv > kMaxCacheRows / Ln) return ATTN_ERR_UNSUPPORTED;
   p.k_in = k;
   p.v_in = v;
   p.new_lens = new_lens;
@@ -1428,7 +1434,7 @@ attn_status_t read_impl(const void* k_codes, const void* v_codes, const uint8_t*
       cache_params(k_codes, v_codes, k_exp, v_exp, kv_lens, B, Hkv, Lk, d, pg, &p);
   if (vs != ATTN_OK) return vs;
   if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return ATTN_ERR_INVALID_ARG;
-  if ((long long)B * Hkv > 0x7fffffffLL / Lk) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)B * Hkv > kMaxCacheRows / Lk) return ATTN_ERR_UNSUPPORTED;
   p.k_out = k;
   p.v_out = v;
   p.err = error_word_for_current_device();

@@ -47,6 +47,7 @@ def test_paged_rejects_on_host(kw, status):
 
 def test_contiguous_rejects_on_host():
     assert call(kp=None) == INV and call(vp=M) == INV and call(Lk=0) == INV
+    assert call(Lp=0x7fffffff) == UNS and call(Lk=0x7fffffff) == UNS
 
 
 def plan(*args):

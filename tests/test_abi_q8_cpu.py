@@ -123,6 +123,9 @@ def test_bad_pages_are_rejected_on_host(call, kw, status):
 def test_lengths_of_a_contiguous_cache():
     assert _append(Lk=0) == INV and _read(Lk=0) == INV and _decode(Lk=0) == INV
     assert _decode(Lk=0x7fffffff) == UNS
+    assert _append(B=1, Hkv=1, Ln=0x7fffffff) == UNS and _read(B=1, Hkv=1, Lk=0x7ffffff0) == UNS
+    # more (sequence, head) pairs times key tiles than the 32-bit line of work holds
+    assert _decode(B=1 << 20, Hq=16, Hkv=16, Lk=1 << 30) == UNS
 
 
 def test_decode_workspace_holds_two_partials_per_cta():
