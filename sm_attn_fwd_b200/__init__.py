@@ -3,7 +3,9 @@
 Argument marshalling only: every step of the computation runs in the CUDA
 library ``_lib/libattn_b200.so``.  PyTorch supplies device memory and the
 current stream.  There is no fallback path: if the library is missing or the
-tensors are not on a CUDA device, the calls raise.
+tensors are not on a CUDA device, the calls raise.  The calls that a serving
+loop makes every step (8-bit cache, its decodes, shared-prefix decode) are
+marshalled in ``csrc/torch_binding.cpp``, the others here through ctypes.
 
 Entry points (same names as the C ABI):
   attn_fwd(q, k, v, ...)                 -> (o, lse)
@@ -20,6 +22,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 import threading
@@ -77,6 +80,7 @@ EXPORTED_SYMBOLS = (
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "_lib", "libattn_b200.so")
+_EXT_PATH = os.path.join(_PKG, "_lib", "attn_torch.so")
 _lock = threading.Lock()
 _lib = None
 
@@ -580,105 +584,38 @@ def attn_decode_splitkv_noalloc(q, k_cache, v_cache, kv_lens, *, scale=None, num
     return o, lse
 
 
-def _check(name, t, dtype, shape, index):
-    """t must be a contiguous CUDA tensor of this type and shape on CUDA device ``index``."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.get_device() == index and t.is_contiguous()):
-        return
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
-    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                     f"got {t.dtype} {tuple(t.shape)}")
+_ext = None
 
 
-# The current stream's handle without building a Stream object (1.2 us of a 10 us call).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+def _native():
+    """The native part of the binding (built first if it is absent and the compilers
+    exist): the calls that a serving loop makes every step check their tensors, allocate
+    and call the library there, in a third to a half of the host time."""
+    global _ext
+    if _ext is None:
+        load_library()
+        with _lock:
+            if not os.path.exists(_EXT_PATH):
+                from . import build as _build
+                _build.build_ext()
+            if _ext is None:
+                spec = importlib.util.spec_from_file_location("attn_torch", _EXT_PATH)
+                ext = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(ext)
+                _ext = ext
+    return _ext
 
 
-def _call(where, fn, index, stream, *args):
-    """fn(*args, stream) on CUDA device ``index`` (the library launches on the current
-    device, so it is made that one); raises AttnError unless it returns ATTN_OK."""
-    if torch.cuda.current_device() != index:
-        with torch.cuda.device(index):
-            return _call(where, fn, index, stream, *args)
-    if stream is not None:
-        handle = stream.cuda_stream
-    elif _raw_stream is not None:
-        handle = _raw_stream(index)
-    else:
-        handle = torch.cuda.current_stream(index).cuda_stream
-    st = fn(*args, handle)
-    if st != ATTN_OK:
-        raise AttnError(st, where)
+def _done(result, where):
+    """A native call's result; AttnError for a status."""
+    if result.__class__ is int:
+        raise AttnError(result, where)
+    return result
 
 
-def _cache_shape(k_cache, block_table):
-    """(batch or None, Hkv, longest sequence, d, page_size, pages_per_seq, num_pages) of an
-    8-bit cache: contiguous when block_table is None, else pages."""
-    if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda:
-        raise ValueError("k_cache must be a CUDA tensor")
-    shape = k_cache.shape
-    if len(shape) != 4:
-        raise ValueError("the cache must have 4 dimensions: [B, Hkv, Lk_max, d], or "
-                         "[num_pages, Hkv, page_size, d] for pages")
-    n, Hkv, rows, d = shape
+def _need_table(block_table):
     if block_table is None:
-        return n, Hkv, rows, d, 0, 0, 0
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be an int32 CUDA tensor [B, pages_per_seq]")
-    B, per_seq = block_table.shape
-    return B, Hkv, rows * per_seq, d, rows, per_seq, n
-
-
-def _check_q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, B):
-    """Checks the tensors of an 8-bit cache; returns their CUDA device's index."""
-    shape = k_cache.shape
-    dev = k_cache.get_device()
-    _check("k_cache", k_cache, torch.float8_e4m3fn, shape, dev)
-    _check("v_cache", v_cache, torch.float8_e4m3fn, shape, dev)
-    _check("k_exp", k_exp, torch.uint8, shape[:3], dev)
-    _check("v_exp", v_exp, torch.uint8, shape[:3], dev)
-    if block_table is not None:
-        _check("block_table", block_table, torch.int32, block_table.shape, dev)
-    _check("kv_lens", kv_lens, torch.int32, (B,), dev)
-    return dev
-
-
-def _check_decode(q, B, d, scale, o, lse, dev):
-    """Checks a decode's queries and outputs (allocated when None): (Hq, Lq, scale, o, lse)."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be a [B, Hq, Lq, d] CUDA tensor")
-    _, Hq, Lq, _ = q.shape
-    _check("q", q, torch.bfloat16, (B, Hq, Lq, d), dev)
-    if o is None:
-        o = torch.empty_like(q)
-    else:
-        _check("o", o, torch.bfloat16, q.shape, dev)
-    if lse is None:
-        lse = q.new_empty((B, Hq, Lq), dtype=torch.float32)
-    else:
-        _check("lse", lse, torch.float32, (B, Hq, Lq), dev)
-    return Hq, Lq, 1.0 / math.sqrt(d) if scale is None else float(scale), o, lse
-
-
-def _workspace(workspace, size_fn, size_args, q, where):
-    """(tensor, bytes) of a workspace, allocated with size_fn(*size_args) bytes when not
-    given."""
-    if workspace is None:
-        if torch.cuda.current_device() != q.get_device():  # the plan goes by its SM count
-            with torch.cuda.device(q.get_device()):
-                need = size_fn(*size_args)
-        else:
-            need = size_fn(*size_args)
-        if need == 0:
-            raise AttnError(ATTN_ERR_INVALID_ARG, where)
-        return q.new_empty(need, dtype=torch.uint8), need
-    if (not isinstance(workspace, torch.Tensor) or workspace.get_device() != q.get_device()
-            or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on {q.device}")
-    return workspace, workspace.numel() * workspace.element_size()
 
 
 def attn_decode_shared_prefix_num_splits(B, Hq, Hkv, Lq, Lp, num_splits=0):
@@ -708,26 +645,10 @@ def attn_decode_shared_prefix(q, k_prefix, v_prefix, k_cache, v_cache, kv_lens, 
     k_cache/v_cache: [B, Hkv, Lk_max, d], the sequences' own keys; kv_lens: [B] int32,
     how many of those each has (0 allowed).  Returns (o, lse).
     """
-    B, Hkv, Lk, d, _, _, _ = _cache_shape(k_cache, None)
-    if not isinstance(k_prefix, torch.Tensor) or k_prefix.dim() != 3:
-        raise ValueError("k_prefix must be a [Hkv, Lp, d] CUDA tensor")
-    Lp = k_prefix.shape[1]
-    dev = k_cache.get_device()
-    for name, t in (("k_prefix", k_prefix), ("v_prefix", v_prefix)):
-        _check(name, t, torch.bfloat16, (Hkv, Lp, d), dev)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check(name, t, torch.bfloat16, (B, Hkv, Lk, d), dev)
-    _check("kv_lens", kv_lens, torch.int32, (B,), dev)
-    Hq, Lq, scale, o, lse = _check_decode(q, B, d, scale, o, lse, dev)
-    lib = _lib or load_library()
-    where = "attn_decode_shared_prefix"
-    ws, ws_bytes = _workspace(workspace, lib.attn_decode_shared_prefix_workspace_size,
-                              (B, Hq, Hkv, Lq, Lp, Lk, d, num_splits), q, where)
-    _call(where, lib.attn_decode_shared_prefix, dev, stream, q.data_ptr(), k_prefix.data_ptr(),
-          v_prefix.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
-          lse.data_ptr(), kv_lens.data_ptr(), B, Hq, Hkv, Lq, Lp, Lk, d, scale, int(num_splits),
-          ws.data_ptr(), ws_bytes)
-    return o, lse
+    return _done((_ext or _native()).shared_prefix(
+        q, k_prefix, v_prefix, None, 0, k_cache, v_cache, None, kv_lens, scale, num_splits,
+        workspace, o, lse, None if stream is None else stream.cuda_stream),
+        "attn_decode_shared_prefix")
 
 
 def attn_decode_shared_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len, block_table,
@@ -740,26 +661,11 @@ def attn_decode_shared_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_le
     ceil(prefix_len / page_size) pages of the prefix; block_table: [B, pages_per_seq]
     int32, the pages of the sequences' own keys.  Returns (o, lse).
     """
-    if block_table is None:
-        raise ValueError("block_table must be an int32 CUDA tensor [B, pages_per_seq]")
-    B, Hkv, Lk, d, page, per_seq, n_pages = _cache_shape(k_pages, block_table)
-    Lp = int(prefix_len)
-    dev = k_pages.get_device()
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        _check(name, t, torch.bfloat16, k_pages.shape, dev)
-    _check("prefix_table", prefix_table, torch.int32, (-(-Lp // max(page, 1)),), dev)
-    _check("block_table", block_table, torch.int32, (B, per_seq), dev)
-    _check("kv_lens", kv_lens, torch.int32, (B,), dev)
-    Hq, Lq, scale, o, lse = _check_decode(q, B, d, scale, o, lse, dev)
-    lib = _lib or load_library()
-    where = "attn_decode_shared_prefix_paged"
-    ws, ws_bytes = _workspace(workspace, lib.attn_decode_shared_prefix_workspace_size,
-                              (B, Hq, Hkv, Lq, Lp, Lk, d, num_splits), q, where)
-    _call(where, lib.attn_decode_shared_prefix_paged, dev, stream, q.data_ptr(),
-          k_pages.data_ptr(), v_pages.data_ptr(), prefix_table.data_ptr(),
-          block_table.data_ptr(), o.data_ptr(), lse.data_ptr(), kv_lens.data_ptr(), B, Hq, Hkv, Lq,
-          Lp, page, per_seq, n_pages, d, scale, int(num_splits), ws.data_ptr(), ws_bytes)
-    return o, lse
+    _need_table(block_table)
+    return _done((_ext or _native()).shared_prefix(
+        q, None, None, prefix_table, prefix_len, k_pages, v_pages, block_table, kv_lens, scale,
+        num_splits, workspace, o, lse, None if stream is None else stream.cuda_stream),
+        "attn_decode_shared_prefix_paged")
 
 
 def attn_cache_append_q8(k, v, k_cache, v_cache, k_exp, v_exp, kv_lens, *, new_lens=None,
@@ -773,7 +679,9 @@ def attn_cache_append_q8(k, v, k_cache, v_cache, k_exp, v_exp, kv_lens, *, new_l
     tokens; new_lens: [B] int32, how many of the Ln rows each sequence gets (all
     when not given).
     """
-    _cache_append(k, v, k_cache, v_cache, k_exp, v_exp, None, kv_lens, new_lens, stream)
+    _done((_ext or _native()).cache_append(
+        k, v, k_cache, v_cache, k_exp, v_exp, None, kv_lens, new_lens,
+        None if stream is None else stream.cuda_stream), "attn_cache_append_q8")
 
 
 def attn_cache_append_paged_q8(k, v, k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, *,
@@ -781,69 +689,29 @@ def attn_cache_append_paged_q8(k, v, k_pages, v_pages, k_exp, v_exp, block_table
     """attn_cache_append_q8 into pages (see ``attn_cache_append_paged_q8`` in
     include/attn.h): k_pages, v_pages [num_pages, Hkv, page_size, d], k_exp, v_exp
     [num_pages, Hkv, page_size], block_table [B, pages_per_seq] int32."""
-    if block_table is None:
-        raise ValueError("block_table must be an int32 CUDA tensor [B, pages_per_seq]")
-    _cache_append(k, v, k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, new_lens, stream)
-
-
-def _cache_append(k, v, k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, new_lens, stream):
-    B, Hkv, Lk, d, page, per_seq, n_pages = _cache_shape(k_cache, block_table)
-    dev = _check_q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, B)
-    if not isinstance(k, torch.Tensor) or k.dim() != 4:
-        raise ValueError("k must be a [B, Hkv, Ln, d] CUDA tensor")
-    Ln = k.shape[2]
-    _check("k", k, torch.bfloat16, (B, Hkv, Ln, d), dev)
-    _check("v", v, torch.bfloat16, (B, Hkv, Ln, d), dev)
-    if new_lens is not None:
-        _check("new_lens", new_lens, torch.int32, (B,), dev)
-        new_lens = new_lens.data_ptr()
-    lib = _lib or load_library()
-    if block_table is None:
-        _call("attn_cache_append_q8", lib.attn_cache_append_q8, dev, stream, k.data_ptr(),
-              v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(),
-              v_exp.data_ptr(), kv_lens.data_ptr(), new_lens, B, Hkv, Ln, Lk, d)
-    else:
-        _call("attn_cache_append_paged_q8", lib.attn_cache_append_paged_q8, dev, stream,
-              k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-              k_exp.data_ptr(), v_exp.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
-              new_lens, B, Hkv, Ln, page, per_seq, n_pages, d)
+    _need_table(block_table)
+    _done((_ext or _native()).cache_append(
+        k, v, k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, new_lens,
+        None if stream is None else stream.cuda_stream), "attn_cache_append_paged_q8")
 
 
 def attn_cache_read_q8(k_cache, v_cache, k_exp, v_exp, kv_lens, *, k=None, v=None, stream=None):
     """The first kv_lens[b] rows of an 8-bit cache as bf16 (see ``attn_cache_read_q8``
     in include/attn.h).  Returns (k, v) [B, Hkv, Lk_max, d] bf16; rows at or past
     kv_lens[b] are left as they are (undefined in tensors allocated here)."""
-    return _cache_read(k_cache, v_cache, k_exp, v_exp, None, kv_lens, k, v, stream)
+    return _done((_ext or _native()).cache_read(
+        k_cache, v_cache, k_exp, v_exp, None, kv_lens, k, v,
+        None if stream is None else stream.cuda_stream), "attn_cache_read_q8")
 
 
 def attn_cache_read_paged_q8(k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, *, k=None,
                              v=None, stream=None):
     """attn_cache_read_q8 from pages (see ``attn_cache_read_paged_q8`` in
     include/attn.h); Lk_max is pages_per_seq * page_size."""
-    if block_table is None:
-        raise ValueError("block_table must be an int32 CUDA tensor [B, pages_per_seq]")
-    return _cache_read(k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, k, v, stream)
-
-
-def _cache_read(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, k, v, stream):
-    B, Hkv, Lk, d, page, per_seq, n_pages = _cache_shape(k_cache, block_table)
-    dev = _check_q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, B)
-    shape = (B, Hkv, Lk, d)
-    k = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) if k is None else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) if v is None else v
-    _check("k", k, torch.bfloat16, shape, dev)
-    _check("v", v, torch.bfloat16, shape, dev)
-    lib = _lib or load_library()
-    if block_table is None:
-        _call("attn_cache_read_q8", lib.attn_cache_read_q8, dev, stream, k_cache.data_ptr(),
-              v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), kv_lens.data_ptr(),
-              k.data_ptr(), v.data_ptr(), B, Hkv, Lk, d)
-    else:
-        _call("attn_cache_read_paged_q8", lib.attn_cache_read_paged_q8, dev, stream,
-              k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(),
-              block_table.data_ptr(), kv_lens.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hkv,
-              page, per_seq, n_pages, d)
-    return k, v
+    _need_table(block_table)
+    return _done((_ext or _native()).cache_read(
+        k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, k, v,
+        None if stream is None else stream.cuda_stream), "attn_cache_read_paged_q8")
 
 
 def attn_decode_q8_workspace_size(Hq, Hkv, Lq, d, num_ctas=0) -> int:
@@ -863,40 +731,19 @@ def attn_decode_splitkv_q8(q, k_cache, v_cache, k_exp, v_exp, kv_lens, *, scale=
     (uint8, attn_decode_q8_workspace_size bytes) is allocated here when not given.
     Returns (o, lse).
     """
-    return _decode_q8(q, k_cache, v_cache, k_exp, v_exp, None, kv_lens, scale, num_ctas,
-                      workspace, o, lse, stream)
+    return _done((_ext or _native()).decode_q8(
+        q, k_cache, v_cache, k_exp, v_exp, None, kv_lens, scale, num_ctas, workspace, o, lse,
+        None if stream is None else stream.cuda_stream), "attn_decode_splitkv_q8")
 
 
 def attn_decode_paged_q8(q, k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, *, scale=None,
                          num_ctas=0, workspace=None, o=None, lse=None, stream=None):
     """attn_decode_splitkv_q8 over pages (see ``attn_decode_paged_q8`` in
     include/attn.h); the cache as for ``attn_cache_append_paged_q8``."""
-    if block_table is None:
-        raise ValueError("block_table must be an int32 CUDA tensor [B, pages_per_seq]")
-    return _decode_q8(q, k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, scale, num_ctas,
-                      workspace, o, lse, stream)
-
-
-def _decode_q8(q, k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, scale, num_ctas,
-               workspace, o, lse, stream):
-    B, Hkv, Lk, d, page, per_seq, n_pages = _cache_shape(k_cache, block_table)
-    dev = _check_q8_cache(k_cache, v_cache, k_exp, v_exp, block_table, kv_lens, B)
-    Hq, Lq, scale, o, lse = _check_decode(q, B, d, scale, o, lse, dev)
-    lib = _lib or load_library()
-    where = "attn_decode_splitkv_q8" if block_table is None else "attn_decode_paged_q8"
-    ws, ws_bytes = _workspace(workspace, lib.attn_decode_q8_workspace_size,
-                              (Hq, Hkv, Lq, d, num_ctas), q, where)
-    if block_table is None:
-        _call(where, lib.attn_decode_splitkv_q8, dev, stream, q.data_ptr(), k_cache.data_ptr(),
-              v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), o.data_ptr(),
-              lse.data_ptr(), kv_lens.data_ptr(), B, Hq, Hkv, Lq, Lk, d, scale, int(num_ctas),
-              ws.data_ptr(), ws_bytes)
-    else:
-        _call(where, lib.attn_decode_paged_q8, dev, stream, q.data_ptr(), k_cache.data_ptr(),
-              v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), block_table.data_ptr(),
-              o.data_ptr(), lse.data_ptr(), kv_lens.data_ptr(), B, Hq, Hkv, Lq, page, per_seq,
-              n_pages, d, scale, int(num_ctas), ws.data_ptr(), ws_bytes)
-    return o, lse
+    _need_table(block_table)
+    return _done((_ext or _native()).decode_q8(
+        q, k_pages, v_pages, k_exp, v_exp, block_table, kv_lens, scale, num_ctas, workspace, o,
+        lse, None if stream is None else stream.cuda_stream), "attn_decode_paged_q8")
 
 
 def attn_selftest_wait_timeout(stream=None):

@@ -1,7 +1,9 @@
 """Ahead-of-time build of the CUDA library for sm_100a (B200).
 
 Compiles ``csrc/*.cu`` with nvcc into ``_lib/libattn_b200.so`` inside the
-package directory (no JIT cache, nothing installed elsewhere).  Run as
+package directory (no JIT cache, nothing installed elsewhere), and
+``csrc/torch_binding.cpp``, the native part of the Python binding, into
+``_lib/attn_torch.so`` beside it.  Run as
 ``python -m sm_attn_fwd_b200.build`` or call :func:`build`.
 """
 from __future__ import annotations
@@ -17,6 +19,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libattn_b200.so")
+EXT = os.path.join(LIBDIR, "attn_torch.so")
+EXT_SOURCE = "torch_binding.cpp"
 SOURCES = ["attn_api.cu", "attn_kernels.cu", "attn_prefill.cu", "attn_short.cu", "attn_noalloc.cu",
            "attn_backward.cu", "attn_cache_q8.cu", "attn_decode_rows.cu",
            "attn_decode_q8_wide.cu", "attn_prefix.cu"]
@@ -98,5 +102,47 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def build_ext(force: bool = False, verbose: bool = False) -> str:
+    """Compile the native part of the binding if its sources, the interpreter or torch
+    changed (it uses torch's C++ interface); return its path."""
+    import sysconfig
+
+    import torch
+
+    lib = build(force, verbose)
+    h = hashlib.sha256(f"{sys.version} {torch.__version__}".encode())
+    for path in (os.path.join(CSRC, EXT_SOURCE), os.path.join(ROOT, "include", "attn.h")):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    digest = h.hexdigest()[:16]
+    stamp = os.path.join(LIBDIR, "attn_torch.sha")
+    if not force and os.path.exists(EXT) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read().strip() == digest:
+                return EXT
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    includes = [os.path.join(t, "include"), os.path.join(cuda, "include"),
+                sysconfig.get_paths()["include"]]
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", os.path.join(ROOT, "include")]
+    for path in includes:
+        cmd += ["-isystem", path]
+    cmd += [os.path.join(CSRC, EXT_SOURCE), "-o", tmp, "-L" + os.path.dirname(lib),
+            "-l:" + os.path.basename(lib), "-Wl,-rpath,$ORIGIN",
+            "-L" + os.path.join(t, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+            "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {EXT_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
+    with open(stamp, "w") as f:
+        f.write(digest)
+    return EXT
+
+
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose=True))
+    print(build_ext(force="--force" in sys.argv))
