@@ -387,8 +387,8 @@ attn_status_t attn_decode_paged_score_mod(const void* q, const void* k_pages, co
  * the partials of the prefix's splits and of the sequences' own caches.  0 for
  * invalid arguments.
  */
-int attn_decode_shared_prefix_num_splits(int B, int Hq, int Hkv, int Lq, int Lp, int num_splits,
-                                         int* chunk_keys);
+int attn_decode_shared_prefix_num_splits(int B, int Hq, int Hkv, int Lq, int Lp, int Lk_max, int d,
+                                         int num_splits, int* chunk_keys);
 size_t attn_decode_shared_prefix_workspace_size(int B, int Hq, int Hkv, int Lq, int Lp, int Lk_max,
                                                 int d, int num_splits);
 

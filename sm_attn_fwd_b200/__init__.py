@@ -150,7 +150,7 @@ def load_library():
                                                     i32, f32, i32, P]
         lib.attn_decode_splitkv_noalloc.restype = i32
         lib.attn_decode_shared_prefix_num_splits.argtypes = \
-            [i32] * 6 + [ctypes.POINTER(ctypes.c_int)]
+            [i32] * 8 + [ctypes.POINTER(ctypes.c_int)]
         lib.attn_decode_shared_prefix_num_splits.restype = i32
         lib.attn_decode_shared_prefix_workspace_size.argtypes = [i32] * 8
         lib.attn_decode_shared_prefix_workspace_size.restype = sz
@@ -618,11 +618,11 @@ def _need_table(block_table):
         raise ValueError("block_table must be an int32 CUDA tensor [B, pages_per_seq]")
 
 
-def attn_decode_shared_prefix_num_splits(B, Hq, Hkv, Lq, Lp, num_splits=0):
+def attn_decode_shared_prefix_num_splits(B, Hq, Hkv, Lq, Lp, Lk_max, d, num_splits=0):
     """(splits, chunk_keys) of the prefix that attn_decode_shared_prefix uses."""
     chunk = ctypes.c_int(0)
-    n = load_library().attn_decode_shared_prefix_num_splits(B, Hq, Hkv, Lq, Lp, num_splits,
-                                                            ctypes.byref(chunk))
+    n = load_library().attn_decode_shared_prefix_num_splits(B, Hq, Hkv, Lq, Lp, Lk_max, d,
+                                                            num_splits, ctypes.byref(chunk))
     if n < 0:
         raise AttnError(ATTN_ERR_INVALID_ARG, "attn_decode_shared_prefix_num_splits")
     return int(n), int(chunk.value)

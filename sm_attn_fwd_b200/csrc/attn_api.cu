@@ -49,7 +49,7 @@ template <int D>
 cudaError_t launch_decode_q8_wide(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
                                   const DecodeParams&, cudaStream_t);
 template <int D>
-cudaError_t launch_decode_merge(const DecodeParams&, cudaStream_t);
+cudaError_t launch_decode_merge(const DecodeParams&, int num_sms, cudaStream_t);
 template <int D>
 cudaError_t launch_prefix(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
                           const PrefixParams&, cudaStream_t);
@@ -1149,10 +1149,27 @@ constexpr int kMaxPrefix = 0x7fffffff - (1 << 20);  // key counters are 32-bit
 struct PrefixPlan {
   int nb, per_seq, tiles, pairs, box_rows;
   int np, chunk;
+  int cache_ctas;  // CTAs for the sequences' own caches
 };
 
-bool plan_prefix(int B, int Hq, int Hkv, int Lq, int Lp, int num_splits, PrefixPlan* pp) {
-  if (B < 1 || Hq < 1 || Hkv < 1 || Lq < 1 || Lp < 1 || num_splits < 0 || Hq % Hkv) return false;
+// How many CTAs work on the prefix, and how many on the sequences' own caches where
+// their decode shares its key tiles out (few query rows).  The two kernels do not
+// depend on each other and take one CTA per SM each, so they either run one after the
+// other on all SMs or, where the prefix's CTAs leave SMs free, side by side: one
+// start-up fewer, and the slower of the two counts.  Costs, in units of one key tile of
+// a prefix CTA (1.9 us at d = 128): the prefix rounds of CTAs over the SMs x (tiles per
+// CTA + 4), the caches 6 + 0.48 per tile of a CTA's share (d = 64: 0.27) counted as
+// decode_sched.cuh does, for full caches; each split's partial rows, written and read
+// back, 0.06 + 1.5e-4 per row.  Side by side the prefix may take at most
+// 1.4 times its least time, which bounds the loss where the caches hold much
+// less.  Measured one after the other / side by side as planned, us: 4 sequences x 8 KV
+// heads, 2064 + 129 keys, d = 128: 17.1 / 13.7; 24 x 4 heads, 8190 + 2064 keys,
+// d = 64, 16 rows: 35.1 / 28.1; 16 x 8 heads, 2064 + 1000 keys: 28.1 / 21.9; 64 x 8
+// heads, 4096 + 256 keys, 8 rows: 45.2 / 39.7.
+bool plan_prefix(int B, int Hq, int Hkv, int Lq, int Lp, int Lk_max, int d, int num_splits,
+                 PrefixPlan* pp) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Lq < 1 || Lp < 1 || Lk_max < 1 || num_splits < 0 || Hq % Hkv)
+    return false;
   if (Lp > kMaxPrefix) return false;
   const long long G = (long long)(Hq / Hkv) * Lq;
   if (G > 0x7fffffffLL / 2) return false;
@@ -1163,29 +1180,64 @@ bool plan_prefix(int B, int Hq, int Hkv, int Lq, int Lp, int num_splits, PrefixP
   pp->tiles = (int)tiles;
   pp->pairs = (int)ceil_div(tiles, 2);
   pp->box_rows = G <= kBlockM ? (int)G * pp->nb : kBlockM;
-  const long long key_tiles = ceil_div(Lp, kBlockN);
+  const long long key_tiles = ceil_div(Lp, kBlockN), sms = num_sms();
   const long long units = (long long)Hkv * pp->pairs;
-  long long np = std::min<long long>(num_splits, key_tiles);
-  if (num_splits == 0) {
-    // The count with the least time in units of one key tile of a CTA: rounds of
-    // CTAs over the SMs times (tiles per CTA + about 4 for its start and end),
-    // plus each split's partial rows, written here and read by the combine
-    // (1 KB per row and split at d = 128, about 1 us per key tile and CTA).
-    const double sms = num_sms(), rows = (double)B * Hq * Lq;
-    double best = 0;
-    const long long most = std::min<long long>(key_tiles, ceil_div(4 * num_sms(), units));
-    for (long long n = 1; n <= most; ++n) {
-      const double cost = (double)ceil_div(units * n, (long long)sms) *
-                              ((double)ceil_div(key_tiles, n) + 4.0) +
-                          (double)n * rows * 1.5e-4;
-      if (n == 1 || cost < best) {
-        best = cost;
-        np = n;
+  const bool shares = attn::decode_tile_rows(d, G) < kBlockM;
+  const double cache_work = (double)B * Hkv *
+                            ((double)ceil_div(Lk_max, kBlockN) + attn::kPieceTiles) *
+                            (d == 64 ? 0.27 : 0.48);
+  const double partials = 0.06 + (double)B * Hq * Lq * 1.5e-4;
+  struct Choice {
+    long long tiles, np, ctas;  // key tiles per split, splits, CTAs of the prefix
+    double prefix;              // its time
+  };
+  auto choice = [&](long long n) {
+    Choice c;
+    c.tiles = ceil_div(key_tiles, n);
+    c.np = ceil_div(key_tiles, c.tiles);
+    c.ctas = units * c.np;
+    c.prefix = (double)ceil_div(c.ctas, sms) * ((double)c.tiles + 4.0) + (double)c.np * partials;
+    return c;
+  };
+  auto in_turn = [&](const Choice& c) {
+    return c.prefix + (shares ? 6.0 + cache_work / (double)sms : 0.0);
+  };
+  auto abreast = [&](const Choice& c) {  // c.ctas < sms
+    const double cache = 6.0 + cache_work / (double)(sms - c.ctas);
+    return std::max(c.prefix, cache) + 0.1 * std::min(c.prefix, cache);
+  };
+  // every count that one round of CTAs holds, and for two to four rounds the largest
+  const long long asked = std::min<long long>(num_splits, key_tiles);
+  const long long one_round = std::max<long long>(std::min(key_tiles, sms / units), 1);
+  Choice best = choice(asked > 0 ? asked : 1);
+  if (asked == 0) {
+    for (long long n = 2; n <= one_round; ++n) {
+      const Choice c = choice(n);
+      if (c.prefix < best.prefix) best = c;
+    }
+    for (long long r = 2; r <= 4; ++r) {
+      const Choice c = choice(std::max<long long>(std::min(key_tiles, r * sms / units), 1));
+      if (c.prefix < best.prefix) best = c;
+    }
+  }
+  bool side = false;
+  if (shares) {
+    double cost = in_turn(best);
+    const double limit = 1.4 * (best.prefix + 5.0) - 5.0;  // 5: the rest of the call
+    for (long long n = asked > 0 ? asked : 1; n <= (asked > 0 ? asked : one_round); ++n) {
+      const Choice c = choice(n);
+      if (c.ctas >= sms) break;
+      const double a = side ? abreast(c) : 1.05 * abreast(c);  // in turn unless clearly better
+      if (c.prefix <= limit && a < cost) {
+        best = c;
+        cost = abreast(c);
+        side = true;
       }
     }
   }
-  pp->chunk = (int)(ceil_div(key_tiles, np) * kBlockN);
-  pp->np = (int)ceil_div(Lp, pp->chunk);
+  pp->chunk = (int)(best.tiles * kBlockN);
+  pp->np = (int)best.np;
+  pp->cache_ctas = (int)(side ? sms - best.ctas : sms);
   return true;
 }
 
@@ -1206,8 +1258,9 @@ struct PrefixCall {
 
 bool plan_prefix_call(int B, int Hq, int Hkv, int Lq, int Lp, int Lk_max, int d, int num_splits,
                       PrefixCall* pc) {
-  if (!plan_prefix(B, Hq, Hkv, Lq, Lp, num_splits, &pc->pp)) return false;
+  if (!plan_prefix(B, Hq, Hkv, Lq, Lp, Lk_max, d, num_splits, &pc->pp)) return false;
   if (!plan_share(Hq, Hkv, Lq, d, 0, &pc->share)) return false;
+  pc->share.num_ctas = pc->pp.cache_ctas;  // the workspace has room for one per SM
   if (!plan_splits(B, Hq, Hkv, Lq, Lk_max, d, 0, &pc->split)) return false;
   if ((long long)B * Hq > 0x7fffffffLL / Lq) return false;
   pc->nrows = (long long)B * Hq * Lq;
@@ -1303,7 +1356,7 @@ attn_status_t shared_prefix_impl(const void* q, const void* k_prefix, const void
     e = d == 64 ? attn::launch_decode_rows<64, false>(ck, cv, sh, st)
                 : attn::launch_decode_rows<128, false>(ck, cv, sh, st);
     if (e != cudaSuccess) return ATTN_ERR_CUDA;
-    e = d == 64 ? attn::launch_decode_merge<64>(sh, st) : attn::launch_decode_merge<128>(sh, st);
+    e = d == 64 ? attn::launch_decode_merge<64>(sh, num_sms(), st) : attn::launch_decode_merge<128>(sh, num_sms(), st);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
   }
 
@@ -1328,10 +1381,10 @@ attn_status_t shared_prefix_impl(const void* q, const void* k_prefix, const void
 
 extern "C" {
 
-int attn_decode_shared_prefix_num_splits(int B, int Hq, int Hkv, int Lq, int Lp, int num_splits,
-                                         int* chunk_keys) {
+int attn_decode_shared_prefix_num_splits(int B, int Hq, int Hkv, int Lq, int Lp, int Lk_max, int d,
+                                         int num_splits, int* chunk_keys) {
   PrefixPlan pp;
-  if (!plan_prefix(B, Hq, Hkv, Lq, Lp, num_splits, &pp)) return -1;
+  if (!plan_prefix(B, Hq, Hkv, Lq, Lp, Lk_max, d, num_splits, &pp)) return -1;
   if (chunk_keys) *chunk_keys = pp.chunk;
   return pp.np;
 }
@@ -1496,8 +1549,8 @@ attn_status_t decode_q8_impl(const void* q, const void* k_codes, const void* v_c
                 : attn::launch_decode_rows<128, true>(tk, tv, p, st);
   }
   if (e != cudaSuccess) return ATTN_ERR_CUDA;
-  e = d == 64 ? attn::launch_decode_merge<64>(p, st)
-              : attn::launch_decode_merge<128>(p, st);
+  e = d == 64 ? attn::launch_decode_merge<64>(p, num_sms(), st)
+              : attn::launch_decode_merge<128>(p, num_sms(), st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

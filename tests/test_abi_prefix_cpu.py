@@ -61,14 +61,18 @@ def test_split_plan_covers_the_prefix():
                            (3, 6, 2, 50)):
         for Lp in (1, 127, 128, 129, 2064, 32768, 100001):
             for ns in (0, 1, 3, 1 << 20):
-                n, chunk = plan(B, Hq, Hkv, Lq, Lp, ns)
-                assert chunk % 128 == 0 and n * chunk >= Lp and (n - 1) * chunk < Lp
-                if ns:
-                    assert n <= ns
-    assert plan(4, 16, 2, 1, 1000, 3) == (3, 384)
-    assert plan(4, 16, 2, 1, 1000, 100) == (8, 128)
-    assert plan(0, 16, 2, 1, 1000, 0)[0] == -1 and plan(4, 15, 2, 1, 1000, 0)[0] == -1
-    assert plan(4, 16, 2, 1, 0, 0)[0] == -1 and plan(4, 16, 2, 1, 10, -1)[0] == -1
+                for Lk, d in ((1, 128), (1000, 64), (1 << 20, 128)):
+                    n, chunk = plan(B, Hq, Hkv, Lq, Lp, Lk, d, ns)
+                    assert chunk % 128 == 0 and n * chunk >= Lp and (n - 1) * chunk < Lp
+                    if ns:
+                        assert n <= ns
+    assert plan(4, 16, 2, 1, 1000, 100, 128, 3) == (3, 384)
+    assert plan(4, 16, 2, 1, 1000, 100, 128, 100) == (8, 128)
+    assert plan(0, 16, 2, 1, 1000, 9, 64, 0)[0] == -1
+    assert plan(4, 15, 2, 1, 1000, 9, 64, 0)[0] == -1
+    assert plan(4, 16, 2, 1, 0, 9, 64, 0)[0] == -1
+    assert plan(4, 16, 2, 1, 10, 0, 64, 0)[0] == -1
+    assert plan(4, 16, 2, 1, 10, 9, 64, -1)[0] == -1
 
 
 def test_workspace_holds_both_parts():
@@ -77,7 +81,7 @@ def test_workspace_holds_both_parts():
     B, Hkv, Lp, Lk = 4, 2, 3000, 700
     for d, Hq, Lq, tile in ((64, 16, 2, 16), (128, 16, 1, 8), (64, 16, 4, 32), (128, 16, 4, 0),
                             (64, 32, 4, 0)):
-        np_, _ = plan(B, Hq, Hkv, Lq, Lp, 5)
+        np_, _ = plan(B, Hq, Hkv, Lq, Lp, Lk, d, 5)
         ns, _ = ab.attn_decode_num_splits(B, Hq, Hkv, Lq, Lk, d)
         rows = B * Hq * Lq
         sms = 148  # without a device
