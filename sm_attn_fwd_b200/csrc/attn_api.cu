@@ -1085,17 +1085,18 @@ int log2_of(int pow2) {
 constexpr int kMaxDecodeCtas = 4096;
 
 struct SharePlan {
-  int num_ctas, tile_rows, row_tiles;
+  int num_ctas, tile_rows, row_tiles, piece;
   size_t part_rows;       // rows of partial results
   size_t lse_off, bytes;  // workspace: O, then the LSEs
 };
 
-bool plan_share(int Hq, int Hkv, int Lq, int d, int num_ctas, SharePlan* pl) {
+bool plan_share(int Hq, int Hkv, int Lq, int d, bool q8, int num_ctas, SharePlan* pl) {
   if (Hq < 1 || Hkv < 1 || Lq < 1 || d < 1 || Hq % Hkv) return false;
   if (num_ctas < 0 || num_ctas > kMaxDecodeCtas) return false;
   const long long rows = (long long)(Hq / Hkv) * Lq;
   pl->num_ctas = num_ctas > 0 ? num_ctas : num_sms();
   pl->tile_rows = attn::decode_tile_rows(d, rows);
+  pl->piece = attn::piece_tiles(d, q8, pl->tile_rows);
   const long long tiles = ceil_div(rows, pl->tile_rows);
   if (tiles * Hkv > 0x7fffffffLL) return false;
   pl->row_tiles = (int)tiles;
@@ -1112,7 +1113,7 @@ bool set_share_shape(attn::DecodeParams* p, const void* q, const int32_t* kv_len
                      const PagedKv& pg) {
   if (Lk_max > 0x7fffffff - 4096) return false;
   if ((long long)B * Hq > 0x7fffffffLL / Lq) return false;
-  const long long unit_cost = ceil_div(Lk_max, kBlockN) + attn::kPieceTiles;
+  const long long unit_cost = ceil_div(Lk_max, kBlockN) + pl.piece;
   if ((long long)B * Hkv > 0x7fffffffLL / pl.row_tiles ||
       (long long)B * Hkv * pl.row_tiles > 0x7fffffffLL / unit_cost)
     return false;
@@ -1129,6 +1130,7 @@ bool set_share_shape(attn::DecodeParams* p, const void* q, const int32_t* kv_len
   p->scale_log2 = (float)((double)scale * 1.4426950408889634074);
   p->num_ctas = pl.num_ctas;
   p->tile_rows = pl.tile_rows;
+  p->piece = pl.piece;
   p->row_tiles = pl.row_tiles;
   p->page_size = pg.page_size;
   p->page_shift = pg.block_table ? log2_of(pg.page_size) : 0;
@@ -1184,7 +1186,8 @@ bool plan_prefix(int B, int Hq, int Hkv, int Lq, int Lp, int Lk_max, int d, int 
   const long long units = (long long)Hkv * pp->pairs;
   const bool shares = attn::decode_tile_rows(d, G) < kBlockM;
   const double cache_work = (double)B * Hkv *
-                            ((double)ceil_div(Lk_max, kBlockN) + attn::kPieceTiles) *
+                            ((double)ceil_div(Lk_max, kBlockN) +
+                             attn::piece_tiles(d, false, attn::decode_tile_rows(d, G))) *
                             (d == 64 ? 0.27 : 0.48);
   const double partials = 0.06 + (double)B * Hq * Lq * 1.5e-4;
   struct Choice {
@@ -1259,7 +1262,7 @@ struct PrefixCall {
 bool plan_prefix_call(int B, int Hq, int Hkv, int Lq, int Lp, int Lk_max, int d, int num_splits,
                       PrefixCall* pc) {
   if (!plan_prefix(B, Hq, Hkv, Lq, Lp, Lk_max, d, num_splits, &pc->pp)) return false;
-  if (!plan_share(Hq, Hkv, Lq, d, 0, &pc->share)) return false;
+  if (!plan_share(Hq, Hkv, Lq, d, false, 0, &pc->share)) return false;
   pc->share.num_ctas = pc->pp.cache_ctas;  // the workspace has room for one per SM
   if (!plan_splits(B, Hq, Hkv, Lq, Lk_max, d, 0, &pc->split)) return false;
   if ((long long)B * Hq > 0x7fffffffLL / Lq) return false;
@@ -1356,7 +1359,8 @@ attn_status_t shared_prefix_impl(const void* q, const void* k_prefix, const void
     e = d == 64 ? attn::launch_decode_rows<64, false>(ck, cv, sh, st)
                 : attn::launch_decode_rows<128, false>(ck, cv, sh, st);
     if (e != cudaSuccess) return ATTN_ERR_CUDA;
-    e = d == 64 ? attn::launch_decode_merge<64>(sh, num_sms(), st) : attn::launch_decode_merge<128>(sh, num_sms(), st);
+    e = d == 64 ? attn::launch_decode_merge<64>(sh, num_sms(), st)
+                : attn::launch_decode_merge<128>(sh, num_sms(), st);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
   }
 
@@ -1510,7 +1514,7 @@ attn_status_t decode_q8_impl(const void* q, const void* k_codes, const void* v_c
     return ATTN_ERR_INVALID_ARG;
   if (!(scale > 0.0f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
   SharePlan pl;
-  if (B < 1 || Lk_max < 1 || !plan_share(Hq, Hkv, Lq, d, num_ctas, &pl))
+  if (B < 1 || Lk_max < 1 || !plan_share(Hq, Hkv, Lq, d, true, num_ctas, &pl))
     return ATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
   attn::DecodeParams p;
@@ -1603,7 +1607,7 @@ attn_status_t attn_cache_read_paged_q8(const void* k_pages, const void* v_pages,
 
 size_t attn_decode_q8_workspace_size(int Hq, int Hkv, int Lq, int d, int num_ctas) {
   SharePlan pl;
-  return plan_share(Hq, Hkv, Lq, d, num_ctas, &pl) ? pl.bytes : 0;
+  return plan_share(Hq, Hkv, Lq, d, true, num_ctas, &pl) ? pl.bytes : 0;
 }
 
 attn_status_t attn_decode_splitkv_q8(const void* q, const void* k_cache, const void* v_cache,

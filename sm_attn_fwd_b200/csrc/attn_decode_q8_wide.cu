@@ -81,7 +81,7 @@ struct WCfg {
   // factors of the keys of a tile, as bf16 exponents: K's 128, then V's
   static constexpr int kOffFactor = kOffMl + 1024;
   static constexpr int kOffMisc = kOffFactor + kFactorSlots * 256;
-  static constexpr int kOffBar = kOffMisc + 32 + kRefSlots * 8;
+  static constexpr int kOffBar = kOffMisc + 40 + kRefSlots * 8;
   static constexpr int kNumBars = 12 + 2 * kFactorSlots + 4 * kRaw + 4 * kStages;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8;
   static constexpr int kSmemAlloc = kSmemBytes + 1024;
@@ -124,7 +124,7 @@ struct Misc {
   int total;
   float2 ref[kRefSlots];  // per tile: 2^(kref - 127), vref - 127
 };
-static_assert(sizeof(Misc) == 32 + kRefSlots * 8, "kOffBar");
+static_assert(sizeof(Misc) == 40 + kRefSlots * 8, "kOffBar");
 
 enum : int {
   kQFull = 0,
@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == 0) {
-    const sched::Share sh = sched::find_share(p.kv_lens, p.B, p.Lk, units, blockIdx.x, gridDim.x, err);
+    const sched::Share sh =
+        sched::find_share(p.kv_lens, p.B, p.Lk, units, p.piece, blockIdx.x, gridDim.x, err);
     const int n = sched::count_tiles(sh, p.kv_lens, p.Lk, units);
     if (lane == 0) {
       misc->share = sh;
@@ -233,7 +234,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = misc->tmem_base;
   const sched::Share& share = misc->share;
   const int total = misc->total;  // key tiles of this CTA
-  //sched::let_next_kernel_launch();
   bool ok = true;
 
   if (warp < 4) {

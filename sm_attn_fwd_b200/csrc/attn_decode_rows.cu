@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(RowCfg<D, NB, kQ8>::kThreads, 1)
       ptx::fence_mbar_init();
     }
     const sched::Share sh =
-        sched::find_share(p.kv_lens, p.B, p.Lk, units, blockIdx.x, gridDim.x, p.err);
+        sched::find_share(p.kv_lens, p.B, p.Lk, units, p.piece, blockIdx.x, gridDim.x, p.err);
     if (lane == 0) {
       *share = sh;
       *abort_flag = 0;
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(256) attn_decode_merge_kernel(const DecodePara
   int all = 0, before = 0;
 #pragma unroll 4
   for (int i = lane; i < p.B; i += 32) {
-    const int n = sched::cost_of(sched::seq_len(p.kv_lens, i, p.Lk));
+    const int n = sched::cost_of(sched::seq_len(p.kv_lens, i, p.Lk), p.piece);
     all += n;
     if (i < b) before += n;
   }
@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(256) attn_decode_merge_kernel(const DecodePara
   // the unit's CTAs c0 .. c1, and how many partial results they left
   int c0 = 0, pieces = 0;
   if (tiles > 0) {
-    const int first = before + unit * (tiles + kPieceTiles) + kPieceTiles;  // the unit's tile 0
+    const int first = before + unit * (tiles + p.piece) + p.piece;  // the unit's tile 0
     const sched::Split split(T, sched::ctas_used(T, p.num_ctas));
     c0 = split.of(first);
     pieces = split.of(first + tiles - 1) - c0 + 1;

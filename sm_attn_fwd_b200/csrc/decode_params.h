@@ -51,11 +51,18 @@ struct DecodeParams {
   int num_ctas;
   int tile_rows;  // query rows of a unit: 8, 16, 32 or 128
   int row_tiles;  // units per (b, kv head): ceil(group * Lq / tile_rows)
+  int piece;      // piece_tiles()
   int page_size, page_shift, pages_per_seq, num_pages;
 };
 
-// Cost, in key tiles, of starting on and finishing a unit (decode_sched.cuh).
-constexpr int kPieceTiles = 3;
+// Cost, in key tiles, of starting on and finishing a unit (decode_sched.cuh).  A tile of
+// an 8-bit cache at d = 64 is half the bytes of any other, so it counts more of them:
+// 16 x 16 heads, 1 to 4099 keys, one row: 28.7 us with 5, 32.1 with 3; a bf16 cache
+// (24 x 4 heads, up to 2064 keys, 16 rows, behind a prefix of 8190): 26.8 us with 5,
+// 25.2 with 3.  At d = 128, 2 to 8 measure alike.
+inline int piece_tiles(int d, bool q8, int tile_rows) {
+  return q8 && d == 64 && tile_rows == 8 ? 5 : 3;
+}
 
 // Query rows per unit for `rows` query rows per KV head.  Up to 16 (32 at d = 64) go
 // through mma.m16n8k16 (attn_decode_rows.cu), the smallest of its tiles that holds them;
