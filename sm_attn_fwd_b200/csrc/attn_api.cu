@@ -1184,6 +1184,7 @@ bool plan_prefix(int B, int Hq, int Hkv, int Lq, int Lp, int Lk_max, int d, int 
   pp->box_rows = G <= kBlockM ? (int)G * pp->nb : kBlockM;
   const long long key_tiles = ceil_div(Lp, kBlockN), sms = num_sms();
   const long long units = (long long)Hkv * pp->pairs;
+  if (units > 0x7fffffffLL) return false;
   const bool shares = attn::decode_tile_rows(d, G) < kBlockM;
   const double cache_work = (double)B * Hkv *
                             ((double)ceil_div(Lk_max, kBlockN) +

@@ -75,6 +75,23 @@ def test_split_plan_covers_the_prefix():
     assert plan(4, 16, 2, 1, 10, 9, 64, -1)[0] == -1
 
 
+def test_split_plan_leaves_sms_to_the_caches_where_that_is_planned():
+    """A short prefix and short caches with few query rows: prefix CTAs on part of the
+    SMs.  However long the caches may get, a prefix CTA's key tiles stay within 1.4 times
+    the fewest (counted with 9 for what they do not change).  Many query rows: the caches
+    go through another kernel, and the plan does not depend on them."""
+    sms = 148
+    if ab.torch.cuda.is_available():
+        sms = ab.torch.cuda.get_device_properties(0).multi_processor_count
+    n, chunk = plan(4, 32, 8, 1, 2064, 129, 128, 0)
+    assert 8 * n <= sms * 2 // 3 and chunk >= 256
+    fewest = plan(4, 32, 8, 1, 2064, 1, 128, 0)[1] // 128
+    for Lk in (1, 129, 5000, 1 << 20):
+        assert plan(4, 32, 8, 1, 2064, Lk, 128, 0)[1] // 128 + 9 <= 1.4 * (max(fewest, 1) + 9)
+    assert plan(8, 64, 2, 4, 9000, 1, 128, 0) == plan(8, 64, 2, 4, 9000, 1 << 20, 128, 0)
+    assert plan(2, 2147483646, 1073741823, 1, 100, 100, 128, 0)[0] >= -1  # no overflow
+
+
 def test_workspace_holds_both_parts():
     """Few query rows per KV head: the prefix's splits, a row per output row and two
     partials per CTA; many: the prefix's splits and the decode's."""
