@@ -70,6 +70,9 @@ namespace {
 
 constexpr float kSlack = 8.0f;        // log2 units a running reference may lag behind
 constexpr float kLn2 = 0.69314718055994530942f;
+// The running references before the first score: finite, so that a block whose scores
+// all overflow to -inf adds 2^(-inf) = 0, not 2^(-inf + inf).
+constexpr float kLowest = -3.0e38f;
 
 // Warps per CTA (one CTA per SM): as many as the registers allow, since a warp's
 // chain of dependent steps per block, not the issue rate, is what more warps hide.
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(RowCfg<D, NB, kQ8>::kThreads, 1)
       for (int mu = 0; mu < kMu; ++mu)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[nb][mu][i] = 0.0f;
-      m[nb][0] = m[nb][1] = R[nb][0] = R[nb][1] = -INFINITY;
+      m[nb][0] = m[nb][1] = R[nb][0] = R[nb][1] = kLowest;
       l[nb][0] = l[nb][1] = 0.0f;
     }
     for (int k0 = w.t0 * 128 + warp * kUnit; k0 < key_end && ok; k0 += kWarps * kUnit) {
@@ -656,11 +659,10 @@ __global__ void __launch_bounds__(RowCfg<D, NB, kQ8>::kThreads, 1)
           for (int i = 0; i < 2; ++i) {
             const float m1 = src[(nb * 6 + i) * 32], R1 = src[(nb * 6 + 2 + i) * 32];
             const float mn = fmaxf(m[nb][i], m1), Rn = fmaxf(R[nb][i], R1);
-            const float mu0 = mn == -INFINITY ? 0.0f : mn, Ru0 = Rn == -INFINITY ? 0.0f : Rn;
-            l[nb][i] = l[nb][i] * ptx::ex2(m[nb][i] - mu0) +
-                       src[(nb * 6 + 4 + i) * 32] * ptx::ex2(m1 - mu0);
-            a0[i] = ptx::ex2(R[nb][i] - Ru0);
-            a1[i] = ptx::ex2(R1 - Ru0);
+            l[nb][i] = l[nb][i] * ptx::ex2(m[nb][i] - mn) +
+                       src[(nb * 6 + 4 + i) * 32] * ptx::ex2(m1 - mn);
+            a0[i] = ptx::ex2(R[nb][i] - Rn);
+            a1[i] = ptx::ex2(R1 - Rn);
             m[nb][i] = mn;
             R[nb][i] = Rn;
           }
@@ -685,21 +687,20 @@ __global__ void __launch_bounds__(RowCfg<D, NB, kQ8>::kThreads, 1)
       const int nb = item / (2 * kMu), i = item / kMu & 1, mu = item % kMu;
       const float* st = merge + (nb * 6 + i) * 32 + lane;
       const float* ov = merge + (NB * 6 + (nb * kMu + mu) * 4 + i) * 32 + lane;
-      float M = -INFINITY, Rm = -INFINITY;
+      float M = kLowest, Rm = kLowest;
 #pragma unroll
       for (int x = 0; x < C::kMergeBufs; ++x)
         if (x < n) {
           M = fmaxf(M, st[x * C::kMergeRegs * 32]);
           Rm = fmaxf(Rm, st[x * C::kMergeRegs * 32 + 64]);
         }
-      const float Mu = M == -INFINITY ? 0.0f : M, Ru = Rm == -INFINITY ? 0.0f : Rm;
       float ls = 0.0f, v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
       for (int x = 0; x < C::kMergeBufs; ++x)
         if (x < n) {
           const int off = x * C::kMergeRegs * 32;
-          ls += st[off + 128] * ptx::ex2(st[off] - Mu);
-          const float a = ptx::ex2(st[off + 64] - Ru);
+          ls += st[off + 128] * ptx::ex2(st[off] - M);
+          const float a = ptx::ex2(st[off + 64] - Rm);
           v0 += a * ov[off];
           v1 += a * ov[off + 64];
         }
@@ -707,7 +708,7 @@ __global__ void __launch_bounds__(RowCfg<D, NB, kQ8>::kThreads, 1)
       for (int x = 4; x < 32; x <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
       const bool have = ok && ls > 0.0f;
       const float inv = have ? 1.0f / ls : 0.0f;
-      const float f = ptx::ex2(Ru - Mu);  // O is in units of 2^R, l in units of 2^m
+      const float f = ptx::ex2(Rm - M);  // O is in units of 2^R, l in units of 2^m
       v0 = v0 * inv * f;
       v1 = v1 * inv * f;
       const int r = nb * 8 + 2 * t + i;
@@ -720,7 +721,7 @@ __global__ void __launch_bounds__(RowCfg<D, NB, kQ8>::kThreads, 1)
         else
           *reinterpret_cast<float2*>((final ? p.own_o : p.ws_o) + to) = make_float2(v0, v1);
         if (mu == 0 && g == 0)
-          (!final ? p.ws_lse : p.own_o ? p.own_lse : p.lse)[at + r] = have ? (Mu + ptx::lg2(ls)) * kLn2 : -INFINITY;
+          (!final ? p.ws_lse : p.own_o ? p.own_lse : p.lse)[at + r] = have ? (M + ptx::lg2(ls)) * kLn2 : -INFINITY;
       }
     }
     if (!ok) break;

@@ -332,3 +332,28 @@ def test_bad_lengths_and_pages_are_flagged():
         torch.cuda.synchronize()
         st, _ = ab.attn_get_device_error()
         assert st == ab.ATTN_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Lq", [1, 4, 16])
+def test_scores_that_overflow_to_minus_infinity_have_no_weight(Lq, d):
+    """The first 200 keys score below fp32's range (2^20 * -2^115 in one column, which the
+    other keys have 0 in), whole blocks, warps and tiles of them; Q's other columns lie
+    2^20 below its largest, well inside what the scaled Q keeps."""
+    B, Hq, Hkv, Lk = 2, 8, 2, 500
+    q, k, v, lens = make(83, B, Hq, Hkv, Lq, Lk, d, [500, 333])
+    q[..., 0] = 2.0 ** 20
+    x = k[2].clone()
+    x[..., 0] = 0
+    x[:, :, :200, 0] = -2.0 ** 115
+    code, e, val = quantise(x)
+    exact = torch.from_numpy(val).to(torch.bfloat16)
+    o, lse = decode(q, (code, e, exact), v, lens)
+    kv = torch.from_numpy(lens - 200).to(torch.int32)
+    kk, vv = exact[:, :, 200:].contiguous(), v[2][:, :, 200:].contiguous()
+    ro, rl = oracle.attn_fwd(q, kk, vv, kv_lens=kv)
+    ra, _ = oracle.attn_fwd(q, kk, vv.abs(), kv_lens=kv)
+    o = o.float().cpu().double().numpy()
+    assert np.isfinite(o).all()
+    assert (np.abs(o - ro) <= 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 2.0 ** -12) * ra).all()
+    assert np.abs(lse.cpu().double().numpy() - rl).max() <= 2e-5

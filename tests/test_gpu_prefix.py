@@ -254,3 +254,30 @@ def test_binding_rejects_wrong_shapes_and_types():
                                      workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
     assert ab.attn_get_device_error()[0] == ab.ATTN_OK
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq", [4, 12, 80])
+def test_scores_that_overflow_to_minus_infinity_have_no_weight(Hq, d):
+    """The first 70 keys of every own cache score below fp32's range (2^83 * -2^83 in one
+    column, which the other keys have 0 in), whole blocks and warps of them."""
+    B, Hkv, Lq, Lp, Lk = 3, 2, 1, 200, 300
+    lens = [300, 70, 131]
+    q, kp, vp, k, v, lens = make(61, B, Hq, Hkv, Lq, Lp, Lk, d, lens)
+    q[..., 0] = 2.0 ** 83
+    kp[..., 0] = 0
+    k[..., 0] = 0
+    k[:, :, :70, 0] = -2.0 ** 83
+    o, lse = run(q, kp, vp, k, v, lens)
+    # the same without those keys
+    k2, v2 = k[:, :, 70:].contiguous(), v[:, :, 70:].contiguous()
+    kk = torch.cat([kp.expand(B, *kp.shape), k2], 2).contiguous()
+    vv = torch.cat([vp.expand(B, *vp.shape), v2], 2).contiguous()
+    kv = torch.from_numpy(np.maximum(lens - 70, 0) + Lp).to(torch.int32)
+    ro, rl = oracle.attn_fwd(q, kk, vv, kv_lens=kv)
+    ra, _ = oracle.attn_fwd(q, kk, vv.abs(), kv_lens=kv)
+    o = o.float().cpu().double().numpy()
+    assert np.isfinite(o).all()
+    assert (np.abs(o - ro) <= 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 2.0 ** -12) * ra).all()
+    # scores of the other keys: at most 10 in magnitude, so 1e-5 + 1e-6 * 10
+    assert np.abs(lse.cpu().double().numpy() - rl).max() <= 2e-5
