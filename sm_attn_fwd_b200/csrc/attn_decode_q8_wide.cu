@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float mu = m == -INFINITY ? 0.0f : m;
       float a0 = ptx::ex2(m_ref - mu), a1 = ptx::ex2(other.x - mu);
       const float sum = a0 * l + a1 * other.y;
-      const bool have = sum > 0.0f;
+      const bool have = sum != 0.0f;  // NaN stays NaN
       const float inv = have ? 1.0f / sum : 0.0f;
       a0 *= inv;
       a1 *= inv;

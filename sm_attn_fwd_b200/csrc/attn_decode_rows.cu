@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(RowCfg<D, NB, kQ8>::kThreads, 1)
         }
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
-      const bool have = ok && ls > 0.0f;
+      const bool have = ok && ls != 0.0f;  // NaN stays NaN
       const float inv = have ? 1.0f / ls : 0.0f;
       const float f = ptx::ex2(Rm - M);  // O is in units of 2^R, l in units of 2^m
       v0 = v0 * inv * f;
@@ -854,7 +854,8 @@ __global__ void __launch_bounds__(256) attn_decode_merge_kernel(const DecodePara
     float m = ls;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (m == -INFINITY) continue;
+    const bool none = m == -INFINITY && !__any_sync(0xffffffffu, ls != ls);  // NaN stays NaN
+    if (none) continue;
     if (m > mx) {  // more than 32 results: what came before counts relative to the new maximum
       const float a = ptx::ex2((mx - m) * kLog2e);
       sum *= a;
@@ -879,14 +880,14 @@ __global__ void __launch_bounds__(256) attn_decode_merge_kernel(const DecodePara
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
   __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + row * D + lane * kPer;
   if constexpr (kPer == 4)
     *reinterpret_cast<uint2*>(dst) = make_uint2(ptx::pack_bf16x2(acc[0] * inv, acc[1] * inv),
                                                 ptx::pack_bf16x2(acc[2] * inv, acc[3] * inv));
   else
     *reinterpret_cast<uint32_t*>(dst) = ptx::pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  if (lane == 0) p.lse[row] = sum > 0.0f ? mx + ptx::lg2(sum) * kLn2 : -INFINITY;
+  if (lane == 0) p.lse[row] = sum != 0.0f ? mx + ptx::lg2(sum) * kLn2 : -INFINITY;
 }
 
 namespace {

@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         row_ok = bi < p.nb && b < p.B;
       }
       const long long out = (long long)split * p.nrows + ((long long)b * p.Hkv + hkv) * p.G + rr;
-      const bool have = ok && l > 0.0f;
+      const bool have = ok && l != 0.0f;  // NaN stays NaN
       const float inv_l = have ? 1.0f / l : 0.0f;
 #pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {

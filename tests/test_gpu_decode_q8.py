@@ -357,3 +357,16 @@ def test_scores_that_overflow_to_minus_infinity_have_no_weight(Lq, d):
     assert np.isfinite(o).all()
     assert (np.abs(o - ro) <= 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 2.0 ** -12) * ra).all()
     assert np.abs(lse.cpu().double().numpy() - rl).max() <= 2e-5
+
+
+@pytest.mark.parametrize("Lq", [1, 4, 16])
+def test_a_nan_query_gives_nan_in_its_row_only(Lq):
+    B, Hq, Hkv, Lk, d = 2, 8, 2, 700, 128
+    q, k, v, lens = make(84, B, Hq, Hkv, Lq, Lk, d, [700, 1])
+    want, want_lse = decode(q, k, v, lens)
+    q[:, 3, Lq - 1, 5] = math.nan
+    o, lse = decode(q, k, v, lens)
+    assert bool(o[:, 3, Lq - 1].isnan().all()) and bool(lse[:, 3, Lq - 1].isnan().all())
+    rest = torch.ones(Hq, Lq, dtype=torch.bool)
+    rest[3, Lq - 1] = False
+    assert torch.equal(o[:, rest], want[:, rest]) and torch.equal(lse[:, rest], want_lse[:, rest])

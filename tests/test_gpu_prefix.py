@@ -281,3 +281,14 @@ def test_scores_that_overflow_to_minus_infinity_have_no_weight(Hq, d):
     assert (np.abs(o - ro) <= 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 2.0 ** -12) * ra).all()
     # scores of the other keys: at most 10 in magnitude, so 1e-5 + 1e-6 * 10
     assert np.abs(lse.cpu().double().numpy() - rl).max() <= 2e-5
+
+
+def test_a_nan_query_gives_nan_in_its_row_only():
+    B, Hq, Hkv, Lq, Lp, Lk, d = 3, 8, 2, 1, 700, 300, 128
+    q, kp, vp, k, v, lens = make(62, B, Hq, Hkv, Lq, Lp, Lk, d, [300, 0, 131])
+    want, want_lse = run(q, kp, vp, k, v, lens)
+    q[:, 3, 0, 5] = math.nan
+    o, lse = run(q, kp, vp, k, v, lens)
+    assert bool(o[:, 3].isnan().all()) and bool(lse[:, 3].isnan().all())
+    rest = [h for h in range(Hq) if h != 3]
+    assert torch.equal(o[:, rest], want[:, rest]) and torch.equal(lse[:, rest], want_lse[:, rest])
