@@ -5,7 +5,7 @@
 // attn_decode_rows.cu keeps up with memory; with 128 rows (16 drafted tokens x 8
 // heads) the products are 16 times larger and belong on tcgen05.  Its operands
 // must lie in shared or tensor memory as 16-bit values, so here the codes are
-// expanded: two warpgroups turn the K and V tiles, as TMA left them, into the bf16
+// expanded: four warpgroups turn the K and V tiles, as TMA left them, into the bf16
 // tiles the bf16 decode would have loaded.
 //
 //   K'_j = kc_j 2^(ke_j - kref),  V'_j = vc_j 2^(ve_j - vref),
@@ -21,25 +21,28 @@
 // 2^(120 + e - ref) finishes them: 4 instructions per pair.  A factor of 0 clears
 // keys past the end, whatever their codes hold (the construction yields no NaN).
 //
-// Roles (640 threads, one CTA per SM, looping over the pieces of its share of the
-// work, decode_sched.cuh): warp 0 loads the codes, in half tiles of 64 keys; warps 1 and 2
-// issue the MMAs of even and odd key tiles (warp 1 also loads Q); warp 3 turns scale
-// bytes into factors (loading them where they are used stalled the expansion 800
-// cycles per tile); warpgroups 1 and 2 are the softmaxes, each with an S
-// and an O of its own in tensor memory; warpgroup 3 expands K tiles and warpgroup 4
-// V tiles (one warpgroup for both took 2700 cycles per tile).  At the end of a piece
+// Roles (896 threads, one CTA per SM, looping over the pieces of its share of the
+// work, decode_sched.cuh): warp 0 loads the codes, in half tiles of 64 keys; warp 1
+// issues the MMAs; warp 2 loads Q; warp 3 turns scale bytes into factors (loading them
+// where they are used stalled the expansion 800 cycles per tile); warpgroups 1 and 2 are
+// the softmaxes, one for the first 64 keys of every tile and one for the last, each with a
+// running maximum and an O of its own in tensor memory, so that they exchange
+// nothing; S is double buffered, the next tile's ready while this one is worked on;
+// warpgroups 3 to 6 expand the halves of the K and the V tiles.  At the end of a piece
 // warpgroup 1 merges the two O and writes the result, while the loads, the expansion
 // and the first S of the next piece go on.
 //
 // What bounds it: per 128-key tile at d = 128 shared memory moves 32 KB of codes in,
 // 32 KB out to the expansion, 64 KB back and 96 KB to the MMAs, 1750 cycles at 128
 // bytes a cycle, against 1400 cycles that the codes take to arrive at the SM's share
-// of the copy bandwidth and 1024 for the exponentials.  What it takes is about 3200
-// cycles: the expansion and the softmax are 1674 instructions per scheduler and tile
-// (52 % of the issue slots), in chains that wait for one another across the roles.
-// Measured: 16 x 8 KV heads x 16384 keys, 128 query rows: 221 us (2.5 TB/s, tensor pipe
-// 32 %); up to 32768 keys in 16-key pages: 313 us where bytes and products each need
-// 104.
+// of the copy bandwidth and 1024 each for the MMAs and the exponentials.  It takes about
+// 2900: a softmax's chain per tile (wait, load of S, maximum, exponentials, store of
+// P) and the expansion's share of the issue slots; with the expansion's arithmetic left
+// out it still takes 94 % of the time.  Measured: 16 x 8 KV heads x 16384 keys, 128 query
+// rows: 208 us (2.6 TB/s); up to 32768 keys in 16-key pages: 296 us, where bytes and
+// products each need 104.  One softmax per even and odd tile, whose S waits for the P V
+// before it, with one expansion warpgroup for K and one for V: 313 us; this one with
+// two expansion warpgroups: 306.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -56,14 +59,14 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 640;
-// registers per thread of the warpgroups: loads and MMAs; softmax (two); expansion of K
-// and of V.  48 + 2 * 176 + 2 * 40 = 5 * 96, the launch's.
+constexpr int kThreads = 896;
+// registers per thread of the warpgroups: loads and MMAs; softmax (two); expansion (four).
+// 48 + 2 * 120 + 4 * 48 <= 7 * 72, the launch's.
 constexpr int kRegsIssue = 48;
-constexpr int kRegsExpand = 40;
-constexpr int kRegsSoftmax = 176;
+constexpr int kRegsExpand = 48;
+constexpr int kRegsSoftmax = 120;
 // more than the launch's registers would wait for ever
-static_assert(kRegsIssue + 2 * kRegsSoftmax + 2 * kRegsExpand <= 5 * 96, "register shares");
+static_assert(kRegsIssue + 2 * kRegsSoftmax + 4 * kRegsExpand <= 7 * 72, "register shares");
 constexpr int kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -87,7 +90,7 @@ struct WCfg {
   static constexpr int kOffFactor = kOffMl + 1024;
   static constexpr int kOffMisc = kOffFactor + kFactorSlots * 256;
   static constexpr int kOffBar = kOffMisc + 40 + kRefSlots * 8;
-  static constexpr int kNumBars = 12 + 2 * kFactorSlots + 4 * kRaw + 4 * kStages;
+  static constexpr int kNumBars = 17 + 2 * kFactorSlots + 4 * kRaw + 4 * kStages;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8;
   static constexpr int kSmemAlloc = kSmemBytes + 1024;
   static_assert(kSmemAlloc <= 227 * 1024, "shared memory");
@@ -95,7 +98,7 @@ struct WCfg {
 
 // 64 of a row's scores: P = 2^(s c - m) as packed bf16 pairs, returning their fp32 sum
 // (row::exp2_pack128 on half a row).
-__device__ __forceinline__ float exp2_pack64(const float (&s)[128], int base, float c, float m,
+__device__ __forceinline__ float exp2_pack64(const float (&s)[64], float c, float m,
                                              uint32_t (&pk)[32]) {
   constexpr int kAhead = 4;
   float e0[kAhead], e1[kAhead];
@@ -112,7 +115,7 @@ __device__ __forceinline__ float exp2_pack64(const float (&s)[128], int base, fl
     }
     if (i < 32) {
       float a0, a1;
-      ptx::fma2_bc(a0, a1, s[base + 2 * i], s[base + 2 * i + 1], c, -m);
+      ptx::fma2_bc(a0, a1, s[2 * i], s[2 * i + 1], c, -m);
       e0[i % kAhead] = ptx::ex2(a0);
       e1[i % kAhead] = ptx::ex2(a1);
     }
@@ -120,6 +123,42 @@ __device__ __forceinline__ float exp2_pack64(const float (&s)[128], int base, fl
 #pragma unroll
   for (int k = 0; k < 4; ++k) sum8[k] += sum8[k + 4];
   return (sum8[0] + sum8[1]) + (sum8[2] + sum8[3]);
+}
+
+// The largest of 64 scores, in 8 chains.
+__device__ __forceinline__ float row_max64(const float (&v)[64]) {
+  float m[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m[j] = fmaxf(v[j], v[8 + j]);
+#pragma unroll
+  for (int i = 16; i < 64; i += 8)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m[j] = fmaxf(m[j], v[i + j]);
+#pragma unroll
+  for (int w = 4; w >= 1; w >>= 1)
+#pragma unroll
+    for (int j = 0; j < w; ++j) m[j] = fmaxf(m[j], m[j + w]);
+  return m[0];
+}
+
+// O (+)= P V over 64 keys: 4 MMAs, P in tensor memory (8 columns per 16 keys), V
+// MN-major in shared memory (2048 bytes per 16 keys).
+__device__ __forceinline__ void mma_pv_chain4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, one;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.u32 one, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.u32 a, %1, 8;   add.s64 b, %2, 128;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, one;\n\t"
+      "add.u32 a, %1, 16;  add.s64 b, %2, 256;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, one;\n\t"
+      "add.u32 a, %1, 24;  add.s64 b, %2, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, one;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 struct Misc {
@@ -133,15 +172,18 @@ static_assert(sizeof(Misc) == 40 + kRefSlots * 8, "kOffBar");
 
 enum : int {
   kQFull = 0,
-  kQEmpty = 1,   // MMA warps (2) -> Q loader: last S of the piece done
-  kSFull = 2,    // [2] MMA -> softmax x
-  kPFull = 4,    // [2] softmax x (128) -> MMA
-  kODone = 6,    // [2] MMA -> softmax x: P V of the tile done
-  kOFree = 8,    // warpgroup 1 (128) -> MMA: both O read out
-  kMlFull = 9,   // warpgroup 2 (128) -> warpgroup 1: (m, l) of the odd tiles
-  kMlEmpty = 10, // warpgroup 1 (128) -> warpgroup 2
-  kDrain = 11,
-  kFactorFull = 12,                           // [kFactorSlots] warp 3 -> expansion
+  kQEmpty = 1,     // MMA -> Q loader: last S of the piece done
+  kSFull = 2,      // [2] MMA -> both softmaxes: S of an even, odd tile
+  // [x][j % 2], as a softmax can be two tiles ahead of the MMA issuer: a barrier's next
+  // phase begins only after the wait for this one
+  kPFull = 4,      // softmax x (128) -> MMA: its half of P written, its O rescaled
+  kODone = 8,      // MMA -> softmax x: its P V of the tile done
+  kOFree = 12,     // warpgroup 1 (128) -> MMA: both O read out
+  kMlFull = 13,    // warpgroup 2 (128) -> warpgroup 1: its (m, l)
+  kMlEmpty = 14,   // warpgroup 1 (128) -> warpgroup 2
+  kDrain = 15,
+  kPieceDone = 16, // MMA -> warpgroup 1: every P V of the piece done
+  kFactorFull = 17,                           // [kFactorSlots] warp 3 -> expansion
   kFactorEmpty = kFactorFull + kFactorSlots,  // [kFactorSlots] expansion (8 warps) -> warp 3
   // raw_full[2][R], raw_empty[2][R] (K's, V's), then full[2][S], empty[2][S] of the expanded
   // tiles
@@ -208,26 +250,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::prefetch_tmap(&tm_k);
       ptx::prefetch_tmap(&tm_v);
       ptx::mbar_init(&bars[kQFull], 1);
-      ptx::mbar_init(&bars[kQEmpty], 2);
-      for (int x = 0; x < 2; ++x) {
-        ptx::mbar_init(&bars[kSFull + x], 1);
-        ptx::mbar_init(&bars[kPFull + x], 128);
-        ptx::mbar_init(&bars[kODone + x], 1);
+      ptx::mbar_init(&bars[kQEmpty], 1);
+      for (int i = 0; i < 2; ++i) ptx::mbar_init(&bars[kSFull + i], 1);
+      for (int i = 0; i < 4; ++i) {
+        ptx::mbar_init(&bars[kPFull + i], 128);
+        ptx::mbar_init(&bars[kODone + i], 1);
       }
       ptx::mbar_init(&bars[kOFree], 128);
       ptx::mbar_init(&bars[kMlFull], 128);
       ptx::mbar_init(&bars[kMlEmpty], 128);
-      ptx::mbar_init(&bars[kDrain], 2);
+      ptx::mbar_init(&bars[kDrain], 1);
+      ptx::mbar_init(&bars[kPieceDone], 1);
       for (int i = 0; i < kFactorSlots; ++i) {
         ptx::mbar_init(&bars[kFactorFull + i], 1);
-        ptx::mbar_init(&bars[kFactorEmpty + i], 8);
+        ptx::mbar_init(&bars[kFactorEmpty + i], 16);
       }
       for (int i = 0; i < 2 * R; ++i) {
         ptx::mbar_init(&bars[kRing + i], 1);
         ptx::mbar_init(&bars[kRing + 2 * R + i], 4);
       }
       for (int i = 0; i < 2 * S; ++i) {
-        ptx::mbar_init(&bars[kRing + 4 * R + i], 128);
+        ptx::mbar_init(&bars[kRing + 4 * R + i], 256);
         ptx::mbar_init(&bars[kRing + 4 * R + 2 * S + i], 1);
       }
       ptx::fence_mbar_init();
@@ -388,71 +431,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
       }
+    } else if (warp == 2) {
+      // ---------------------------------------------------------- Q of each piece
+      int piece = 0;
+      sched::Walk w;
+      for (w.start(share, p.kv_lens, p.Lk); w.valid(); w.next(p.kv_lens, p.Lk, units), ++piece) {
+        ok = ptx::mbar_wait_a(BAR(kQEmpty), ((uint32_t)piece & 1u) ^ 1u, abort_flag, err,
+                              kDevErrTimeoutProducer);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          const int hkv = w.h / p.row_tiles, rt = w.h - hkv * p.row_tiles;
+          const int rows_all = p.group * p.Lq;
+          const int y = (w.b * p.Hkv + hkv) * rows_all + rt * 128;
+          ptx::mbar_arrive_expect_tx(&bars[kQFull], C::kTileBytes);
+          for (int a = 0; a < C::kAtoms; ++a)
+            ptx::tma_load_2d(smem + C::kOffQ + a * C::kAtomBytes, &tm_q, &bars[kQFull], a * 64, y);
+        }
+        __syncwarp();
+      }
+      if (piece > 0 && lane == 0) {  // the last Q has landed
+        int dummy = 0;
+        ptx::mbar_wait_a(BAR(kQFull), (uint32_t)(piece - 1) & 1u, &dummy, nullptr, 0);
+      }
     } else {
-      // ------------------------------- MMA issuer of the tiles of parity x
-      const int x = warp - 1;
+      // ------------------------------------------------------------ MMA issuer
+      // S of tile j goes to buffer j % 2, two tiles ahead of its softmax; P lies over S,
+      // so S of tile j + 2 follows tile j's P V in pipe order.
       constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(128, 128, 0, 0);
       constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(128, D, 0, 1);
-      const uint32_t s_tmem = tmem + (x ? 128u : 0u);
-      const uint32_t o_tmem = tmem + 256u + (uint32_t)(x * D);
       const uint64_t q_desc = ptx::smem_desc_sw128(sq, 16, 1024);
       auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
         const bool r = ptx::mbar_wait_a(bar, parity, abort_flag, err, kDevErrTimeoutMma);
         return __all_sync(0xffffffffu, r);
       };
-      int base = 0;   // tiles of the earlier pieces
-      int n = 0;      // own tiles done
+      int base = 0;  // tiles of the earlier pieces
       int piece = 0;
       sched::Walk w;
       for (w.start(share, p.kv_lens, p.Lk); w.valid() && ok;
            w.next(p.kv_lens, p.Lk, units), ++piece) {
         const int end = base + w.t1 - w.t0;
-        if (x == 0) {
-          ok = wait(BAR(kQEmpty), ((uint32_t)piece & 1u) ^ 1u);
-          if (!ok) break;
-          if (lane == 0) {
-            const int hkv = w.h / p.row_tiles, rt = w.h - hkv * p.row_tiles;
-            const int rows_all = p.group * p.Lq;
-            const int y = (w.b * p.Hkv + hkv) * rows_all + rt * 128;
-            ptx::mbar_arrive_expect_tx(&bars[kQFull], C::kTileBytes);
-            for (int a = 0; a < C::kAtoms; ++a)
-              ptx::tma_load_2d(smem + C::kOffQ + a * C::kAtomBytes, &tm_q, &bars[kQFull], a * 64,
-                               y);
-          }
-          __syncwarp();
-        }
-        ok = wait(BAR(kQFull), (uint32_t)piece & 1u);
-        const int first = base + ((x ^ base) & 1);
         auto issue_s = [&](int j) -> bool {
           const int st = j % S;
           if (!wait(FULL(0, st), (uint32_t)(j / S) & 1u)) return false;
           ptx::tc_fence_after();
+          const uint32_t s_tmem = tmem + (uint32_t)(j & 1) * 128u;
           const uint64_t k_desc = ptx::smem_desc_sw128(sk + st * C::kTileBytes, 16, 1024);
           if constexpr (D == 64)
             ptx::mma_qk_chain_d64(s_tmem, q_desc, k_desc, kIdescS);
           else
             ptx::mma_qk_chain_d128(s_tmem, q_desc, k_desc, kIdescS);
-          ptx::mma_commit_warp(BAR(kSFull + x));
+          ptx::mma_commit_warp(BAR(kSFull + (j & 1)));
           ptx::mma_commit_warp(EMPTY(0, st));
-          if (j + 2 >= end) ptx::mma_commit_warp(BAR(kQEmpty));
+          if (j + 1 == end) ptx::mma_commit_warp(BAR(kQEmpty));
           return true;
         };
-        if (ok && first < end) ok = issue_s(first);
-        if (first >= end) ptx::mma_commit_warp(BAR(kQEmpty));  // no tile of this parity
-        for (int j = first; j < end && ok; j += 2, ++n) {
+        ok = wait(BAR(kQFull), (uint32_t)piece & 1u) && issue_s(base);
+        if (ok && base + 1 < end) ok = issue_s(base + 1);
+        for (int j = base; j < end && ok; ++j) {
           const int st = j % S;
-          ok = wait(BAR(kPFull + x), (uint32_t)n & 1u) &&
-               wait(FULL(1, st), (uint32_t)(j / S) & 1u);
-          if (ok && j == first && piece > 0)  // the previous piece's O has been read out
+          const uint32_t s_tmem = tmem + (uint32_t)(j & 1) * 128u;
+          const uint64_t v_desc =
+              ptx::smem_desc_sw128(sv_ + st * C::kTileBytes, C::kAtomBytes, 1024);
+          ok = wait(FULL(1, st), (uint32_t)(j / S) & 1u);
+          if (ok && j == base && piece > 0)  // the previous piece's O have been read out
             ok = wait(BAR(kOFree), (uint32_t)(piece - 1) & 1u);
+          for (int x = 0; x < 2 && ok; ++x) {
+            ok = wait(BAR(kPFull + 2 * x + (j & 1)), (uint32_t)(j >> 1) & 1u);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            mma_pv_chain4(tmem + 256u + (uint32_t)(x * D), s_tmem + (uint32_t)(x * 64),
+                          v_desc + (uint64_t)(x * 512), kIdescPV, j > base ? 1u : 0u);
+            ptx::mma_commit_warp(BAR(kODone + 2 * x + (j & 1)));
+          }
           if (!ok) break;
-          ptx::tc_fence_after();
-          ptx::mma_pv_chain8(o_tmem, s_tmem,
-                             ptx::smem_desc_sw128(sv_ + st * C::kTileBytes, C::kAtomBytes, 1024),
-                             kIdescPV, j > first ? 1u : 0u);
-          ptx::mma_commit_warp(BAR(kODone + x));
           ptx::mma_commit_warp(EMPTY(1, st));
-          // the next S overwrites P: behind this P V, in pipe order
+          if (j + 1 == end) ptx::mma_commit_warp(BAR(kPieceDone));
           if (j + 2 < end) ok = issue_s(j + 2);
         }
         base = end;
@@ -460,92 +514,82 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mma_commit_warp(BAR(kDrain));
       int dummy = 0;
       ptx::mbar_wait_a(BAR(kDrain), 0, &dummy, nullptr, 0);
-      if (x == 0 && piece > 0 && lane == 0) {  // the last Q has landed
-        dummy = 0;
-        ptx::mbar_wait_a(BAR(kQFull), (uint32_t)(piece - 1) & 1u, &dummy, nullptr, 0);
-      }
     }
   } else if (warp >= 12) {
     // ------------------------------------------------------------- expansion
-    // Warp w of the warpgroup takes rows 16 w .. + 15 of each half tile; a thread
-    // takes 16 codes of a row at a time, eight lanes on eight neighbouring rows
+    // A warpgroup per operand and half tile; warp w of it takes rows 16 w .. + 15; a
+    // thread takes 16 codes of a row at a time, eight lanes on eight neighbouring rows
     // (conflict-free in both swizzled layouts).
     ptx::regs_dec<kRegsExpand>();
     constexpr int kH = D / 64;  // 16-code chunks per thread and row
-    const int kv = (warp - 12) >> 2;
+    const int kv = (warp - 12) >> 3;
+    const int half = (warp - 12) >> 2 & 1;  // of each tile
     const int row_w = (warp & 3) * 16 + (lane & 7);  // and + 8
     for (int j = 0; j < total; ++j) {
       const int st = j % S, fs = j % kFactorSlots;
       const uint32_t dst = (kv ? sv_ : sk) + st * C::kTileBytes;
       const uint8_t* factor = smem + C::kOffFactor + fs * 256 + kv * 128;
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        const int hj = 2 * j + half, slot = hj % R;
-        const uint32_t src = ptx::smem_u32(smem + C::kOffRaw + (kv * R + slot) * C::kRawBytes);
-        if (half == 0)
-          ok = ptx::mbar_wait_a(BAR(kFactorFull + fs), (uint32_t)(j / kFactorSlots) & 1u,
-                                abort_flag, err, kDevErrTimeoutProducer);
-        ok = ok && ptx::mbar_wait_a(RAW_FULL(kv, slot), (uint32_t)(hj / R) & 1u, abort_flag, err,
-                                    kDevErrTimeoutProducer);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        // all loads first, so that they are in flight together
-        uint32_t w[2][kH][4], f[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = row_w + 8 * i;
-          f[i] = (uint32_t)factor[half * 64 + r] * 0x00800080u;
-#pragma unroll
-          for (int h = 0; h < kH; ++h) {
-            const int q = (lane >> 3) + 4 * h;  // 16-code chunk of the row
-            const uint32_t from = D == 128 ? (uint32_t)(r * 128 + ((q ^ (r & 7)) << 4))
-                                           : (uint32_t)(r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
-            ptx::ld_shared_v4(src + from, w[i][h][0], w[i][h][1], w[i][h][2], w[i][h][3]);
-          }
-        }
-        if (half == 0) {
-          ok = ptx::mbar_wait_a(EMPTY(kv, st), ((uint32_t)(j / S) & 1u) ^ 1u, abort_flag, err,
-                                kDevErrTimeoutProducer);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = half * 64 + row_w + 8 * i;
-#pragma unroll
-          for (int h = 0; h < kH; ++h) {
-            const int q = (lane >> 3) + 4 * h;
-            uint32_t o[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              // bytes (b, sign b, b', sign b') of two neighbouring codes
-              uint32_t x;
-              asm("prmt.b32 %0, %1, 0, %2;"
-                  : "=r"(x)
-                  : "r"(w[i][h][k >> 1]), "r"(k & 1 ? 0xb3a2 : 0x9180));
-              const uint32_t v = (x << 4) & 0x87f087f0u;
-              const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                               *reinterpret_cast<const __nv_bfloat162*>(&f[i]));
-              o[k] = *reinterpret_cast<const uint32_t*>(&y);
-            }
-            // 16 values: chunks 2 (q % 4) and + 1 of atom q / 4
-            const uint32_t row = dst + (uint32_t)((q >> 2) * C::kAtomBytes + r * 128);
-            const int ch = (q & 3) * 2;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             row + (uint32_t)((ch ^ (r & 7)) << 4)),
-                         "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                         : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             row + (uint32_t)(((ch + 1) ^ (r & 7)) << 4)),
-                         "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-                         : "memory");
-          }
-        }
-        // the codes are in registers or stored: their slot may be loaded again
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_a(RAW_EMPTY(kv, slot));
-      }
+      const int hj = 2 * j + half, slot = hj % R;
+      const uint32_t src = ptx::smem_u32(smem + C::kOffRaw + (kv * R + slot) * C::kRawBytes);
+      ok = ptx::mbar_wait_a(BAR(kFactorFull + fs), (uint32_t)(j / kFactorSlots) & 1u, abort_flag,
+                            err, kDevErrTimeoutProducer) &&
+           ptx::mbar_wait_a(RAW_FULL(kv, slot), (uint32_t)(hj / R) & 1u, abort_flag, err,
+                            kDevErrTimeoutProducer);
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
+      // all loads first, so that they are in flight together
+      uint32_t w[2][kH][4], f[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = row_w + 8 * i;
+        f[i] = (uint32_t)factor[half * 64 + r] * 0x00800080u;
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+          const int q = (lane >> 3) + 4 * h;  // 16-code chunk of the row
+          const uint32_t from = D == 128 ? (uint32_t)(r * 128 + ((q ^ (r & 7)) << 4))
+                                         : (uint32_t)(r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+          ptx::ld_shared_v4(src + from, w[i][h][0], w[i][h][1], w[i][h][2], w[i][h][3]);
+        }
+      }
+      ok = ptx::mbar_wait_a(EMPTY(kv, st), ((uint32_t)(j / S) & 1u) ^ 1u, abort_flag, err,
+                            kDevErrTimeoutProducer);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = half * 64 + row_w + 8 * i;
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+          const int q = (lane >> 3) + 4 * h;
+          uint32_t o[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            // bytes (b, sign b, b', sign b') of two neighbouring codes
+            uint32_t x;
+            asm("prmt.b32 %0, %1, 0, %2;"
+                : "=r"(x)
+                : "r"(w[i][h][k >> 1]), "r"(k & 1 ? 0xb3a2 : 0x9180));
+            const uint32_t v = (x << 4) & 0x87f087f0u;
+            const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&f[i]));
+            o[k] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          // 16 values: chunks 2 (q % 4) and + 1 of atom q / 4
+          const uint32_t row = dst + (uint32_t)((q >> 2) * C::kAtomBytes + r * 128);
+          const int ch = (q & 3) * 2;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           row + (uint32_t)((ch ^ (r & 7)) << 4)),
+                       "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                       : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           row + (uint32_t)(((ch + 1) ^ (r & 7)) << 4)),
+                       "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                       : "memory");
+        }
+      }
+      // the codes are in registers or stored: their slot may be loaded again
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_a(RAW_EMPTY(kv, slot));
       ptx::fence_proxy_async_smem();
       ptx::mbar_arrive_a(FULL(kv, st));
       if (lane == 0) ptx::mbar_arrive_a(BAR(kFactorEmpty + fs));
@@ -557,7 +601,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;  // row of the unit = TMEM lane
     const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t s_col = x ? 128u : 0u;
     const uint32_t o_col = 256u + (uint32_t)(x * D);
     float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
@@ -565,30 +608,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       return __all_sync(0xffffffffu, a);
     };
     int base = 0;  // tiles of the earlier pieces
-    // barrier parities, in one register: own tiles done (bit 0), odd tiles of the earlier
-    // pieces (bit 1), pieces done (bit 2); bit 3: a piece is done
-    uint32_t ph = 0;
+    int piece = 0;
     sched::Walk w;
     for (w.start(share, p.kv_lens, p.Lk); w.valid() && ok;
-         w.next(p.kv_lens, p.Lk, units), ph = (ph ^ 4u) | 8u) {
+         w.next(p.kv_lens, p.Lk, units), ++piece) {
       const int end = base + w.t1 - w.t0;
-      const int first = base + ((x ^ base) & 1);
       const int key_end = min(w.t1 * 128, w.len);
       float m_ref = -INFINITY, l = 0.0f;
-      for (int j = first; j < end; j += 2, ph ^= 1u) {
-        const int left = key_end - (w.t0 + j - base) * 128;  // keys of the tile below the end
-        ok = wait(BAR(kSFull + x), ph & 1u);
+      for (int j = base; j < end; ++j) {
+        // keys of this half tile below the end
+        const int left = key_end - (w.t0 + j - base) * 128 - x * 64;
+        ok = wait(BAR(kSFull + (j & 1)), (uint32_t)(j >> 1) & 1u);
         if (!ok) break;
         ptx::tc_fence_after();
         const float2 ref = misc->ref[j % kRefSlots];
         const float c = p.scale_log2 * ref.x;
-        float s[128];
-        row::tmem_ld_row128(t_row + s_col, s);
-        if (left < 128) {
+        const uint32_t s_col = t_row + (uint32_t)((j & 1) * 128 + x * 64);
+        float s[64];
+        {
+          uint32_t r0[32], r1[32];
+          ptx::tmem_ld32(s_col, r0);
+          ptx::tmem_ld32(s_col + 32, r1);
+          ptx::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 128; ++i) s[i] = i < left ? s[i] : -INFINITY;
+          for (int i = 0; i < 32; ++i) {
+            s[i] = __uint_as_float(r0[i]);
+            s[32 + i] = __uint_as_float(r1[i]);
+          }
         }
-        const float m_new = fmaxf(m_ref, ptx::row_max128(s) * c);
+        if (left < 64) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) s[i] = i < left ? s[i] : -INFINITY;
+        }
+        const float m_new = fmaxf(m_ref, row_max64(s) * c);
         const bool need = m_new > m_ref + kRescaleThreshold;
         const float alpha = need ? ptx::ex2(m_ref - m_new) : 1.0f;
         if (need) {
@@ -596,9 +648,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           m_ref = m_new;
         }
         const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
-        if (j > first && __any_sync(0xffffffffu, need)) {
-          // O holds the P V of the warpgroup's earlier tiles: final before it is rescaled
-          ok = wait(BAR(kODone + x), ~ph & 1u);
+        if (j > base && __any_sync(0xffffffffu, need)) {
+          // O holds the P V of the piece's earlier tiles: final before it is rescaled
+          ok = wait(BAR(kODone + 2 * x + ((j - 1) & 1)), (uint32_t)((j - 1) >> 1) & 1u);
           if (!ok) break;
           ptx::tc_fence_after();
 #pragma unroll 1
@@ -611,35 +663,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tmem_st32(t_row + o_col + cc * 32, raw);
           }
         }
-        // P' over S in two halves: the first half's registers are free for the second
-        float sum = 0.0f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
-          sum += exp2_pack64(s, h * 64, c, m_use - ref.y, pk);
-          ptx::tmem_st32(t_row + s_col + h * 32, pk);
-        }
+        uint32_t pk[32];  // P' over this half of S
+        const float sum = exp2_pack64(s, c, m_use - ref.y, pk);
+        ptx::tmem_st32(s_col, pk);
         l += sum * ptx::ex2(-ref.y);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
-        ptx::mbar_arrive_a(BAR(kPFull + x));
+        ptx::mbar_arrive_a(BAR(kPFull + 2 * x + (j & 1)));
       }
       if (!ok) break;
       // ------------------------------------------------------- end of the piece
-      const int odd = (end >> 1) - (base >> 1);  // odd tiles of the piece
-      ph ^= (uint32_t)(odd & 1) << 1;
-      const bool has_even = end - base > odd, has_odd = odd > 0;
       base = end;
       if (x == 1) {
-        if (ph & 8u) ok = wait(BAR(kMlEmpty), ~ph >> 2 & 1u);
+        if (piece > 0) ok = wait(BAR(kMlEmpty), (uint32_t)(piece - 1) & 1u);
         if (!ok) break;
         ml[r] = make_float2(m_ref, l);
         ptx::mbar_arrive_a(BAR(kMlFull));
         continue;
       }
-      ok = (!has_even || wait(BAR(kODone), ~ph & 1u)) &&
-           (!has_odd || wait(BAR(kODone + 1), ~ph >> 1 & 1u)) &&
-           wait(BAR(kMlFull), ph >> 2 & 1u);
+      ok = wait(BAR(kPieceDone), (uint32_t)piece & 1u) &&
+           wait(BAR(kMlFull), (uint32_t)piece & 1u);
       if (!ok) break;
       ptx::tc_fence_after();
       const float2 other = ml[r];
@@ -662,12 +705,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 : (long long)w.slot(blockIdx.x) * 128 + r;
 #pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {
-        // an O that no tile of the piece wrote holds anything: it is not read
         uint32_t e[32], o[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) e[i] = o[i] = 0u;
-        if (has_even) ptx::tmem_ld32(t_row + 256u + cc * 32, e);
-        if (has_odd) ptx::tmem_ld32(t_row + 256u + D + cc * 32, o);
+        ptx::tmem_ld32(t_row + 256u + cc * 32, e);
+        ptx::tmem_ld32(t_row + 256u + D + cc * 32, o);
         ptx::tmem_wait_ld();
         if (row_ok) {
           float v[32];
