@@ -292,6 +292,8 @@ size_t attn_decode_workspace_size(int B, int Hq, int Hkv, int Lq, int Lk_max, in
  * across CTAs, then merged): (1) per (b, kv head, split) a partial O_s and
  * LSE_s over that chunk, for all Hq/Hkv query heads of the group at once;
  * (2) the combine LSE = log sum_s exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s.
+ * A NaN score (a NaN in the query or in a key below kv_lens[b]) makes O and LSE of
+ * its row NaN; a NaN value makes its column of O NaN.
  *
  * Arguments
  *   q        [B, Hq, Lq, d] bf16, read
@@ -403,6 +405,8 @@ size_t attn_decode_shared_prefix_workspace_size(int B, int Hq, int Hkv, int Lq, 
  * attn_decode_splitkv on the concatenation.  The prefix is read once for the
  * whole batch, its query rows stacked into 128-row tiles across sequences; three
  * launches on `stream`: the prefix's partials, the caches' partials, the combine.
+ * NaN in queries, keys and values as in attn_decode_splitkv.  Scores and sums are
+ * fp32, and P is rounded to bf16 for its product with V, as there.
  *
  * Arguments
  *   q        [B, Hq, Lq, d] bf16, read;  o [B, Hq, Lq, d] bf16, lse [B, Hq, Lq]

@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       ptx::tc_fence_after();
     }
-    const bool have = ok && n_tiles > 0 && l > 0.0f;
+    const bool have = ok && n_tiles > 0 && l != 0.0f;  // NaN stays NaN
     const float inv_l = have ? 1.0f / l : 0.0f;
     const float lse_row = have ? (m_ref + ptx::lg2(l)) * kLn2 : -INFINITY;
     const long long out_row = row_out0 + r;
@@ -566,8 +566,13 @@ __global__ void __launch_bounds__(256) attn_decode_combine_kernel(const FwdParam
   // every split wrote this row's LSE (-inf where it held no key of the sequence)
   const int ns = p.nsplit;
   float mx = -INFINITY;
+  bool nan = false;  // which the maximum passes over
   for (int s0 = 0; s0 < ns; s0 += 32) {
-    if (s0 + lane < ns) mx = fmaxf(mx, p.ws_lse[(long long)(s0 + lane) * nrows + row]);
+    if (s0 + lane < ns) {
+      const float ls = p.ws_lse[(long long)(s0 + lane) * nrows + row];
+      mx = fmaxf(mx, ls);
+      nan |= ls != ls;
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -575,7 +580,7 @@ __global__ void __launch_bounds__(256) attn_decode_combine_kernel(const FwdParam
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
   float sum = 0.0f;
-  if (mx != -INFINITY) {
+  if (mx != -INFINITY || __any_sync(0xffffffffu, nan)) {
     for (int s0 = 0; s0 < ns; s0 += 32) {
       // lane i: weight of split s0 + i (0 for a split with no visible key)
       const float ls = s0 + lane < ns ? p.ws_lse[(long long)(s0 + lane) * nrows + row] : -INFINITY;
@@ -614,7 +619,7 @@ __global__ void __launch_bounds__(256) attn_decode_combine_kernel(const FwdParam
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;  // NaN stays NaN
   __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + row * D + lane * kPer;
   if constexpr (kPer == 4) {
     uint2 o2;
@@ -624,7 +629,7 @@ __global__ void __launch_bounds__(256) attn_decode_combine_kernel(const FwdParam
   } else {
     *reinterpret_cast<uint32_t*>(dst) = ptx::pack_bf16x2(acc[0] * inv, acc[1] * inv);
   }
-  if (lane == 0) p.lse[row] = sum > 0.0f ? mx + ptx::lg2(sum) * kLn2 : -INFINITY;
+  if (lane == 0) p.lse[row] = sum != 0.0f ? mx + ptx::lg2(sum) * kLn2 : -INFINITY;
 }
 
 // Failure-detection self-test: one thread waits, with the same bounded wait the
