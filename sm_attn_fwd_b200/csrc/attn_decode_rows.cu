@@ -708,9 +708,11 @@ __global__ void __launch_bounds__(RowCfg<D, NB, kQ8>::kThreads, 1)
       for (int x = 4; x < 32; x <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
       const bool have = ok && ls != 0.0f;  // NaN stays NaN
       const float inv = have ? 1.0f / ls : 0.0f;
-      const float f = ptx::ex2(Rm - M);  // O is in units of 2^R, l in units of 2^m
-      v0 = v0 * inv * f;
-      v1 = v1 * inv * f;
+      // O is in units of 2^R, l in units of 2^m.  In two factors: with the smallest value
+      // scales 2^(R - m) is no normal number, and ex2 would give 0.
+      const float f = ptx::ex2(0.5f * (Rm - M));
+      v0 = v0 * inv * f * f;
+      v1 = v1 * inv * f * f;
       const int r = nb * 8 + 2 * t + i;
       if (r < rows_valid) {
         const int col = kQ8 ? g * (D / 8) + 2 * mu : (mu >> 2) * 64 + g * 8 + 2 * (mu & 3);
