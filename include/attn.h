@@ -553,8 +553,10 @@ size_t attn_decode_q8_workspace_size(int Hq, int Hkv, int Lq, int d, int num_cta
  *   O_i = sum_j softmax_j(S_ij) 2^(v_exp_j - 127) vc_j,  LSE_i = log sum_j exp(S_ij).
  * The codes reach the tensor cores as exact 16-bit values; scores and sums are
  * fp32.  P is rounded to 16 bits: with up to 16 query rows per KV head (32 at
- * d = 64) to f16 relative to the row's largest P 2^v_exp, so that what a key adds
- * below 2^-24 of the row's largest term may be lost; with more rows to bf16.  Codes and scale bytes at or past kv_lens[b] may hold anything; a NaN code
+ * d = 64) P 2^v_exp to f16, by at most 2^-11 of itself or 2^-32 of the row's largest
+ * P 2^v_exp, whichever is more (n keys may thus lose n 2^-32 of it together, times their
+ * codes); with more rows to bf16, by at most 2^-8.
+ * Codes and scale bytes at or past kv_lens[b] may hold anything; a NaN code
  * below it gives unspecified values in its sequence's rows.  A sequence with
  * kv_lens[b] = 0 gets O = 0 and LSE = -inf.
  *

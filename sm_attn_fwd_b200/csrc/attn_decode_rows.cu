@@ -29,11 +29,14 @@
 // Numbers, 8-bit cache.  Q is scaled per row by a power of two into f16's upper range
 // (an element keeps all 8 bits of its bf16 significand down to 2^-31 of the row's
 // largest).  Scores, maxima and sums are fp32.  P times the value scale goes into
-// the second product as f16 relative to a running reference of its own, R_i >=
-// max_j (S_ij log2 e + ve_j) - 8, separate from the softmax's reference m_i: a
-// value row with a large scale but a small weight then costs the others nothing.
-// f16 rounds P to 11 bits, 8 times finer than bf16.  bf16 cache: both products take
-// bf16 as it is, P rounded to it, and R_i = m_i.
+// the second product as f16 relative to a running reference of its own, R_i between
+// w_i - 15 and w_i - 7, w_i = max_j (S_ij log2 e + ve_j), separate from the softmax's
+// reference m_i: a value row with a large scale but a small weight then costs the others
+// nothing.  f16 rounds P to 11 bits, 8 times finer than bf16, and its largest P is 2^7
+// to 2^15, so that half its smallest step, what a key with next to no weight may lose, is
+// at most 2^-32 of the row's largest P 2^ve.  (Most keys of a long context are such keys:
+// with R_i = w_i a flat tail of weights below 2^-25 vanished, however long.)  bf16 cache:
+// both products take bf16 as it is, P rounded to it, and R_i = m_i.
 //
 // Layout of a warp's block (32 keys; 16 for bf16 at d = 128) in groups of 16 keys.  A
 // contraction does not care about the order of its terms, so d and the keys are
@@ -69,6 +72,9 @@ namespace attn {
 namespace {
 
 constexpr float kSlack = 8.0f;        // log2 units a running reference may lag behind
+// 8-bit cache: how far R lies below the largest P 2^ve, in log2 units.  With the lag P
+// stays at or below 2^15, inside f16's range.
+constexpr float kHeadroom = 7.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 // The running references before the first score: finite, so that a block whose scores
 // all overflow to -inf adds 2^(-inf) = 0, not 2^(-inf + inf).
@@ -517,7 +523,8 @@ __global__ void __launch_bounds__(RowCfg<D, NB, kQ8>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           need |= max_z(nb, i) > m[nb][i] + kSlack;
-          if constexpr (kQ8) need |= max_w(nb, i) > R[nb][i] + kSlack;
+          // (a difference, as a sum is rounded where scores are large, and P must not pass 2^15)
+          if constexpr (kQ8) need |= max_w(nb, i) - R[nb][i] > kSlack + kHeadroom;
         }
       if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
@@ -530,7 +537,7 @@ __global__ void __launch_bounds__(RowCfg<D, NB, kQ8>::kThreads, 1)
               zm = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, x));
               if constexpr (kQ8) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, x));
             }
-            if constexpr (!kQ8) wm = zm;
+            wm = kQ8 ? wm - kHeadroom : zm;
             if (zm > m[nb][i]) {
               l[nb][i] *= ptx::ex2(m[nb][i] - zm);
               m[nb][i] = zm;
