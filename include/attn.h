@@ -556,9 +556,9 @@ size_t attn_decode_q8_workspace_size(int Hq, int Hkv, int Lq, int d, int num_cta
  * d = 64) P 2^v_exp to f16, by at most 2^-11 of itself or 2^-32 of the row's largest
  * P 2^v_exp, whichever is more (n keys may thus lose n 2^-32 of it together, times their
  * codes); with more rows to bf16, by at most 2^-8.
- * Codes and scale bytes at or past kv_lens[b] may hold anything; a NaN code
- * below it gives unspecified values in its sequence's rows.  A sequence with
- * kv_lens[b] = 0 gets O = 0 and LSE = -inf.
+ * Codes and scale bytes at or past kv_lens[b] may hold anything.  Below it a NaN code
+ * of a key makes O and LSE of the rows that see it NaN, one of a value its column of O.
+ * A sequence with kv_lens[b] = 0 gets O = 0 and LSE = -inf.
  *
  * All sequences' key tiles are shared out evenly among num_ctas CTAs (0: one per SM
  * of the current device; a smaller number leaves SMs to other streams), wherever

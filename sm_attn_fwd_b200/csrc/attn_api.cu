@@ -1526,6 +1526,8 @@ attn_status_t decode_q8_impl(const void* q, const void* k_codes, const void* v_c
   p.lse = lse;
   p.ws_o = reinterpret_cast<float*>(workspace);
   p.ws_lse = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + pl.lse_off);
+  p.k_codes = k_codes;
+  p.v_codes = v_codes;
   p.k_exp = k_exp;
   p.v_exp = v_exp;
   p.err = error_word_for_current_device();

@@ -41,6 +41,8 @@ struct DecodeParams {
   float* own_o;             // fp32 [B*Hq*Lq, d]
   float* own_lse;           // fp32 [B*Hq*Lq]
   int num_prefix;
+  const void* k_codes;  // 8-bit cache: codes and scale bytes
+  const void* v_codes;
   const uint8_t* k_exp;
   const uint8_t* v_exp;
   const int32_t* kv_lens;
