@@ -454,8 +454,8 @@ attn_status_t attn_decode_shared_prefix_paged(
  * the pages: the serving-side form of the cache the decode reads.)
  *
  * A cached row (one token of one KV head, d values) is d e4m3 codes (one byte
- * each) and one scale byte e; the row's values are code * 2^(e - 127).  Rows lie
- * as in the bf16 caches:
+ * each) and one scale byte e; the row's values are code * 2^(e - 127).  (Bytes above
+ * 247, which no bf16 row gets, count as 247.)  Rows lie as in the bf16 caches:
  *   k_cache, v_cache  [B, Hkv, Lk_max, d] codes, 16-byte aligned, and
  *   k_exp, v_exp      [B, Hkv, Lk_max] scale bytes, or
  *   k_pages, v_pages  [num_pages, Hkv, page_size, d] codes and

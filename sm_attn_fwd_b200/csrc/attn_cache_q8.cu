@@ -202,8 +202,8 @@ __global__ void __launch_bounds__(kCacheThreads) attn_cache_read_kernel(const Ca
     if (src < 0) continue;  // reads as zeros
     kc[u] = __ldcs(reinterpret_cast<const uint2*>(p.k_codes) + src * kLanes + part);
     vc[u] = __ldcs(reinterpret_cast<const uint2*>(p.v_codes) + src * kLanes + part);
-    ke[u] = __ldg(p.k_exp + src);
-    ve[u] = __ldg(p.v_exp + src);
+    ke[u] = min((int)__ldg(p.k_exp + src), q8::kMaxScaleByte);
+    ve[u] = min((int)__ldg(p.v_exp + src), q8::kMaxScaleByte);
   }
   const long long out0 = (long long)bh * p.Lk * kLanes + part;
 #pragma unroll

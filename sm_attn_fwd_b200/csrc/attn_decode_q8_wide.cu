@@ -55,6 +55,7 @@
 #include <cstdint>
 
 #include "attn_params.h"
+#include "cache_q8.cuh"
 #include "decode_params.h"
 #include "host_once.h"
 #include "ptx.cuh"
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return (int)__reduce_max_sync(0xffffffffu, __vmaxu4(w, w >> 8) & 0xffu);
       };
       // bf16 exponents of 2^(120 + e - ref); 0 (a factor of zero) for e = 0 (past the
-      // end) and underflow.  At most 254: ref >= e - 7.
+      // end) and underflow.  At most 254: e <= 247 and ref >= e - 7.
       auto factors = [](uint32_t w, int ref) -> uint32_t {
         uint32_t r = 0;
 #pragma unroll
@@ -451,7 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kAhead; ++i, ++j) {
           if (j >= total) break;
-          const uint32_t kw = k[i] & live[i], vw = v[i] & live[i];
+          constexpr uint32_t kMax4 = (uint32_t)q8::kMaxScaleByte * 0x01010101u;
+          const uint32_t kw = __vminu4(k[i] & live[i], kMax4);
+          const uint32_t vw = __vminu4(v[i] & live[i], kMax4);
           load(f, i);
           f = fetch();
           const int kref = byte_max(kw);

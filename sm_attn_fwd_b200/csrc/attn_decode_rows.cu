@@ -279,8 +279,8 @@ __global__ void __launch_bounds__(RowCfg<D, NB, kQ8>::kThreads, 1)
   // the scale bytes of block i
   auto store_exps = [&](int i, int ke, int ve) {
     uint8_t* dst = exps + i % S * 64;
-    dst[lane] = (uint8_t)ke;
-    dst[32 + lane] = (uint8_t)ve;
+    dst[lane] = (uint8_t)min(ke, q8::kMaxScaleByte);
+    dst[32 + lane] = (uint8_t)min(ve, q8::kMaxScaleByte);
   };
   // Issue the boxes of the next block (one per operand, or one per page slice for pages
   // shorter than a block), load its scale bytes and find the block after it.

@@ -6,7 +6,9 @@
 // A power of two keeps every step exact except the rounding to e4m3 itself: the
 // division by the scale, the code times the scale, and the scale's use as a
 // factor of a score.  e4m3 is a floating-point format, so a free scale would buy
-// no mantissa bits, only up to one binade at the bottom of the range.
+// no mantissa bits, only up to one binade at the bottom of the range.  No bf16 row needs
+// a byte above 247 (448 * 2^120 passes bf16's largest value); larger ones, which a cache
+// filled by other means may hold, count as 247.
 #pragma once
 
 #include <cstdint>
@@ -15,6 +17,8 @@
 
 namespace attn {
 namespace q8 {
+
+constexpr int kMaxScaleByte = 247;
 
 // Scale byte of a row with largest magnitude amax (finite, >= 0): the smallest
 // e >= 1 with amax <= 448 * 2^(e - 127).  448 = 1.75 * 2^8, so with amax =

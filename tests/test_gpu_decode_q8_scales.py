@@ -7,12 +7,12 @@ import torch
 import oracle
 import sm_attn_fwd_b200 as ab
 from tests.q8_helpers import as_codes
-from tests.test_gpu_decode_q8 import decode
+from tests.test_gpu_decode_q8 import check, decode, make
 
 pytestmark = pytest.mark.gpu
 
-# query tokens of 8 heads over one KV head: 8 and 16 rows
-TOKENS = [1, 2]
+# query tokens of 8 heads over one KV head: 8, 16, 24, 40 and 128 rows
+TOKENS = [1, 2, 3, 5, 16]
 
 
 def codes_of(values, shape, seed):
@@ -24,7 +24,7 @@ def codes_of(values, shape, seed):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("Lq", TOKENS)
+@pytest.mark.parametrize("Lq", [1, 2])
 def test_scale_byte_0_is_2_to_the_minus_127(Lq, d):
     """Values of about 2^-124, and keys of that size under queries of about 2^100 (an 8-bit
     score is q times code in fp32 before its scale).  P in bf16 or better, O in bf16, fp32
@@ -51,3 +51,45 @@ def test_scale_byte_0_is_2_to_the_minus_127(Lq, d):
     kr, vr = ab.attn_cache_read_q8(*(as_codes(x[0]).cuda() for x in (k, v)),
                                    *(torch.from_numpy(x[1]).cuda() for x in (k, v)), kv.cuda())
     assert torch.equal(kr.cpu(), k[2]) and torch.equal(vr.cpu(), v[2])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Lq", TOKENS)
+def test_scale_bytes_above_247_count_as_247(Lq, d):
+    """No bf16 row needs a byte above 247; larger ones count as 247 everywhere, and reach no
+    other key."""
+    B, Hq, Hkv, Lk = 1, 8, 1, 300
+    q, k, v, lens = make(105, B, Hq, Hkv, Lq, Lk, d, [Lk])
+    at = [3, 64, 130, 299]
+    for x in (k, v):
+        x[0][0, 0, at] = 0x01            # 2^-9: values of 2^111
+        x[0][0, 0, at, ::2] = 0x81
+    got = []
+    for bytes_ in ([247] * 4, [248, 250, 254, 255]):
+        vv = (v[0], v[1].copy())
+        vv[1][0, 0, at] = bytes_
+        kk = (k[0], k[1].copy())
+        kk[1][0, 0, at[0]] = bytes_[0]
+        both = [as_codes(k[0]).cuda(), as_codes(v[0]).cuda(), torch.from_numpy(kk[1]).cuda(),
+                torch.from_numpy(vv[1]).cuda(), torch.tensor([Lk], dtype=torch.int32).cuda()]
+        got.append(list(decode(q, k, vv, lens)) + list(decode(q, kk, v, lens)) +
+                   list(ab.attn_cache_read_q8(*both)))
+    for a, b in zip(*got):
+        assert torch.equal(a.cpu().view(torch.int16), b.cpu().view(torch.int16))
+    assert bool(got[0][0].isfinite().all())
+    assert float(got[0][5][0, 0, 3, 1]) == 2.0 ** 111
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Lq", [5, 16])
+def test_a_zero_row_with_any_scale_byte_is_zero(Lq, d):
+    """Many query rows: a value row whose codes are all 0 adds nothing whatever its byte is,
+    and its neighbours keep their values."""
+    q, k, v, lens = make(106, 1, 8, 1, Lq, 300, d, [300])
+    at = [0, 62, 63, 128, 298]
+    v[0][0, 0, at] = 0
+    v[2][0, 0, at] = 0
+    for byte in (1, 246, 247, 248, 251, 252, 255):
+        v[1][0, 0, at] = byte
+        o, lse = decode(q, k, v, lens)
+        check(o, lse, q, k, v, lens)
