@@ -428,14 +428,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         w = __vmaxu4(w, w >> 16);
         return (int)__reduce_max_sync(0xffffffffu, __vmaxu4(w, w >> 8) & 0xffu);
       };
-      // bf16 exponents of 2^(120 + e - ref); 0 (a factor of zero) for e = 0 (past the
-      // end) and underflow.  At most 254: e <= 247 and ref >= e - 7.
-      auto factors = [](uint32_t w, int ref) -> uint32_t {
+      // bf16 exponents of 2^(120 + e - ref); 0 (a factor of zero) past the end only.  At
+      // most 254: e <= 247 and ref >= e - 7.  (The least, 1, is for scales 2^246 below the
+      // reference's: its products underflow.)
+      auto factors = [](uint32_t w, uint32_t alive, int ref) -> uint32_t {
         uint32_t r = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int e = (int)(w >> (8 * i) & 0xffu);
-          if (e > 0) r |= (uint32_t)max(247 + e - ref, 0) << (8 * i);
+          if (alive >> (8 * i) & 1u) r |= (uint32_t)max(247 + e - ref, 1) << (8 * i);
         }
         return r;
       };
@@ -455,9 +456,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr uint32_t kMax4 = (uint32_t)q8::kMaxScaleByte * 0x01010101u;
           const uint32_t kw = __vminu4(k[i] & live[i], kMax4);
           const uint32_t vw = __vminu4(v[i] & live[i], kMax4);
+          const uint32_t alive = live[i];
           load(f, i);
           f = fetch();
-          const int kref = byte_max(kw);
+          const int kref = max(byte_max(kw), 1);
           // vref is bounded so that P' = p 2^(vref - 127) stays clear of both ends of fp32
           const int vref = min(max(byte_max(vw), 67), 240);
           const int fs = j % kFactorSlots;
@@ -466,11 +468,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           uint32_t* out = reinterpret_cast<uint32_t*>(smem + C::kOffFactor + fs * 256);
-          out[lane] = factors(kw, kref);
-          out[32 + lane] = factors(vw, vref);
+          out[lane] = factors(kw, alive, kref);
+          out[32 + lane] = factors(vw, alive, vref);
           if (lane == 0)
             misc->ref[j % kRefSlots] =
-                make_float2(__uint_as_float((uint32_t)max(kref, 1) << 23), (float)(vref - 127));
+                make_float2(__uint_as_float((uint32_t)kref << 23), (float)(vref - 127));
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive_a(BAR(kFactorFull + fs));
         }
