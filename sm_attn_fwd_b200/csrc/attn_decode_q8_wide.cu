@@ -686,7 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         ptx::tc_fence_after();
         const float2 ref = misc->ref[j % kRefSlots];
-        const float c = p.scale_log2 * ref.x;
+        // not 0 where it underflows (keys of the smallest scales): -inf * 0 is NaN
+        const float c = fmaxf(p.scale_log2 * ref.x, 0x1p-149f);
         const uint32_t s_col = t_row + (uint32_t)((j & 1) * 128 + x * 64);
         float s[64];
         {
