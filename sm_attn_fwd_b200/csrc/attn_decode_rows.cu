@@ -874,6 +874,9 @@ __global__ void __launch_bounds__(256) attn_decode_merge_kernel(const DecodePara
     }
     const float wl = ptx::ex2((ls - mx) * kLog2e);  // 0 for -inf
     sum += wl;
+    // a result without keys has no row (anything may lie there); one whose weight only
+    // underflows has, and a NaN in it counts
+    const uint32_t live = __ballot_sync(0xffffffffu, ls != -INFINITY);
     const int k = min(32, n - s0);
     for (int i0 = 0; i0 < k; i0 += kBatch) {
       if (i0 > 0) load(s0 + i0);
@@ -881,9 +884,9 @@ __global__ void __launch_bounds__(256) attn_decode_merge_kernel(const DecodePara
       for (int u = 0; u < kBatch; ++u) {
         if (i0 + u >= k) break;
         const float wi = __shfl_sync(0xffffffffu, wl, i0 + u);
-        // a result without keys has no row (anything may lie there)
+        const bool has = live >> (i0 + u) & 1u;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[i] += wi != 0.0f ? wi * v[u][i] : 0.0f;
+        for (int i = 0; i < kPer; ++i) acc[i] += has ? wi * v[u][i] : 0.0f;
       }
     }
   }

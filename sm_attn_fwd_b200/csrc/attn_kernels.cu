@@ -586,6 +586,8 @@ __global__ void __launch_bounds__(256) attn_decode_combine_kernel(const FwdParam
       const float ls = s0 + lane < ns ? p.ws_lse[(long long)(s0 + lane) * nrows + row] : -INFINITY;
       const float w_lane = ls == -INFINITY ? 0.0f : ptx::ex2((ls - mx) * kLog2e);
       sum += w_lane;
+      // (a split whose weight only underflows takes part: a NaN in its row counts)
+      const uint32_t live = __ballot_sync(0xffffffffu, ls != -INFINITY);
       const int n = min(32, ns - s0);
       for (int i0 = 0; i0 < n; i0 += kUnroll) {
         float wv[kUnroll];
@@ -593,7 +595,7 @@ __global__ void __launch_bounds__(256) attn_decode_combine_kernel(const FwdParam
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
           wv[u] = __shfl_sync(0xffffffffu, w_lane, (i0 + u) & 31);
-          const bool use = i0 + u < n && wv[u] != 0.0f;
+          const bool use = i0 + u < n && (live >> ((i0 + u) & 31) & 1u);
           const float* src =
               p.ws_o + ((long long)(s0 + i0 + u) * nrows + row) * D + lane * kPer;
           if constexpr (kPer == 4) {

@@ -1,8 +1,11 @@
 """NaN codes in the 8-bit cache below its length, through the decode with few query rows per
 KV head and with many."""
+import math
+
 import pytest
 import torch
 
+from tests.q8_helpers import quantise
 from tests.test_gpu_decode_q8 import decode, make
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +46,28 @@ def test_nan_codes_give_nan(Lq, d, page, ctas):
             o, lse = decode(q, k, vn, lens, page, ctas)
             same_bits_but(o, want, column)
             assert torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Lq", TOKENS)
+def test_a_nan_value_counts_where_its_weight_underflows(Lq, d):
+    """Keys 300 below the others in their score, as the second piece of a unit that two CTAs
+    share: the weight of the whole piece is 0 in fp32, and 0 times NaN is NaN."""
+    q, k, v, lens = make(102, 1, 8, 1, Lq, 1024, d, [1024])
+    q[..., 0] = 8
+    x = k[2].clone()
+    x[..., 0] = 0
+    x[:, :, 512:] = 0
+    x[:, :, 512:, 0] = -300 / 8 * math.sqrt(d)
+    code, e, val = quantise(x)
+    k = (code, e, torch.from_numpy(val).to(torch.bfloat16))
+    want, want_lse = decode(q, k, v, lens, 0, 2)
+    v[0][0, 0, 1000, 17] = 0x7F
+    column = torch.zeros(1, 8, Lq, d, dtype=torch.bool)
+    column[..., 17] = True
+    for ctas in (2, 1, 0):
+        o, lse = decode(q, k, v, lens, 0, ctas)
+        assert torch.equal(o.isnan().cpu(), column)
+    o, lse = decode(q, k, v, lens, 0, 2)
+    same_bits_but(o, want, column)
+    assert torch.equal(lse, want_lse)

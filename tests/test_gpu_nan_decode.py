@@ -87,3 +87,24 @@ def test_split_kv(Hq, Lq, d, splits):
     same_bits_but(o, want, nan[..., None].expand(o.shape))
     same_bits_but(lse, want_lse, nan)
     assert ab.attn_get_device_error() == (ab.ATTN_OK, 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Lq", ROWS)
+def test_a_nan_value_counts_where_its_weight_underflows(Hq, Lq, d):
+    """Keys 300 below the others in their score, in a split or in a cache of their own: the
+    weight of the whole partial result is 0 in fp32, and 0 times NaN is NaN."""
+    q, kp, vp, k, v, _ = make(73, 1, Hq, HKV, Lq, 256, 256, d, [256])
+    q[..., 0], kp[..., 0], k[..., 0] = 8, 0, -300 / 8 * math.sqrt(d)
+    want, want_lse = run(q, kp, vp, k, v, np.asarray([256], np.int32))
+    v[0, 1, 200, 9] = math.nan
+    column = torch.zeros(want.shape, dtype=torch.bool)
+    column[:, Hq // HKV:, :, 9] = True
+    o, lse = run(q, kp, vp, k, v, np.asarray([256], np.int32))
+    same_bits_but(o, want, column)
+    assert torch.equal(lse, want_lse)
+    kk, vv = torch.cat([kp[None], k], 2).cuda(), torch.cat([vp[None], v], 2).cuda()
+    kv = torch.tensor([512], dtype=torch.int32, device="cuda")
+    o, _ = ab.attn_decode_splitkv(q.cuda(), kk, vv, kv, num_splits=2)
+    assert torch.equal(o.isnan().cpu(), column)
+    assert ab.attn_get_device_error() == (ab.ATTN_OK, 0)
