@@ -349,6 +349,8 @@ __global__ void __launch_bounds__(RowCfg<D, NB, kQ8>::kThreads, 1)
     float fac0[NB], fac1[NB];  // scale * log2 e * 2^(row shift) of query rows 2t and 2t + 1
     ok = ok && ptx::mbar_wait_a(ptx::smem_u32(&q_bars[piece & 1]), (uint32_t)(piece >> 1) & 1u,
                                 abort_flag, p.err, kDevErrTimeoutProducer);
+    // lanes may give up apart from each other, and the votes below need them all
+    ok = __all_sync(0xffffffffu, ok);
     const uint4* q_s =
         reinterpret_cast<const uint4*>(smem + C::kOffQ + (piece & 1) * (C::kRows * D * 2));
     if constexpr (!kQ8) {
