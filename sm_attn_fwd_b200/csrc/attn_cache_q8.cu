@@ -158,7 +158,7 @@ __device__ __forceinline__ uint4 restore8(const uint2& c, int e) {
     r[i] = *reinterpret_cast<const uint32_t*>(&y);
   }
   if (e > 134) {
-    const uint32_t f2 = (uint32_t)e << 7 | (uint32_t)e << 23;
+    const uint32_t x2 = (uint32_t)min(e, q8::kMaxScaleByte), f2 = x2 << 7 | x2 << 23;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r[i]),
@@ -202,8 +202,8 @@ __global__ void __launch_bounds__(kCacheThreads) attn_cache_read_kernel(const Ca
     if (src < 0) continue;  // reads as zeros
     kc[u] = __ldcs(reinterpret_cast<const uint2*>(p.k_codes) + src * kLanes + part);
     vc[u] = __ldcs(reinterpret_cast<const uint2*>(p.v_codes) + src * kLanes + part);
-    ke[u] = min((int)__ldg(p.k_exp + src), q8::kMaxScaleByte);
-    ve[u] = min((int)__ldg(p.v_exp + src), q8::kMaxScaleByte);
+    ke[u] = __ldg(p.k_exp + src);
+    ve[u] = __ldg(p.v_exp + src);
   }
   const long long out0 = (long long)bh * p.Lk * kLanes + part;
 #pragma unroll

@@ -424,21 +424,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < f.n; ++i) w |= (uint32_t)__ldg(src + i) << (8 * i);
         return w;
       };
-      auto byte_max = [](uint32_t w) -> int {
-        w = __vmaxu4(w, w >> 16);
-        return (int)__reduce_max_sync(0xffffffffu, __vmaxu4(w, w >> 8) & 0xffu);
+      // Caps the four bytes of w and returns the largest one of the warp's; in 16-bit halves,
+      // which have minimum and maximum instructions.
+      auto cap_and_max = [](uint32_t& w) -> int {
+        constexpr uint32_t kMax2 = (uint32_t)q8::kMaxScaleByte * 0x00010001u;
+        const uint32_t even = __vminu2(w & 0x00ff00ffu, kMax2);
+        const uint32_t odd = __vminu2(w >> 8 & 0x00ff00ffu, kMax2);
+        w = even | odd << 8;
+        const uint32_t m = __vmaxu2(even, odd);
+        return (int)__reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
       };
-      // bf16 exponents of 2^(120 + e - ref); 0 (a factor of zero) past the end only.  At
-      // most 254: e <= 247 and ref >= e - 7.  (The least, 1, is for scales 2^246 below the
-      // reference's: its products underflow.)
+      // bf16 exponents of 2^(120 + e - ref), 247 + e - ref, of four keys; 0 (a factor of
+      // zero) past the end only.  One addition: no byte carries or becomes 0, as
+      // e <= 247, e - 7 <= ref <= 246.
       auto factors = [](uint32_t w, uint32_t alive, int ref) -> uint32_t {
-        uint32_t r = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = (int)(w >> (8 * i) & 0xffu);
-          if (alive >> (8 * i) & 1u) r |= (uint32_t)max(247 + e - ref, 1) << (8 * i);
-        }
-        return r;
+        return (w + (uint32_t)(247 - ref) * 0x01010101u) & alive;
       };
       uint32_t k[kAhead], v[kAhead], live[kAhead];  // live: mask of the live keys' bytes
       auto load = [&](const Tile& f, int i) {
@@ -453,15 +453,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kAhead; ++i, ++j) {
           if (j >= total) break;
-          constexpr uint32_t kMax4 = (uint32_t)q8::kMaxScaleByte * 0x01010101u;
-          const uint32_t kw = __vminu4(k[i] & live[i], kMax4);
-          const uint32_t vw = __vminu4(v[i] & live[i], kMax4);
+          uint32_t kw = k[i] & live[i], vw = v[i] & live[i];
           const uint32_t alive = live[i];
           load(f, i);
           f = fetch();
-          const int kref = max(byte_max(kw), 1);
+          const int kref = min(max(cap_and_max(kw), 1), 246);
           // vref is bounded so that P' = p 2^(vref - 127) stays clear of both ends of fp32
-          const int vref = min(max(byte_max(vw), 67), 240);
+          const int vref = min(max(cap_and_max(vw), 67), 240);
           const int fs = j % kFactorSlots;
           ok = ptx::mbar_wait_a(BAR(kFactorEmpty + fs), ((uint32_t)(j / kFactorSlots) & 1u) ^ 1u,
                                 abort_flag, err, kDevErrTimeoutProducer);
