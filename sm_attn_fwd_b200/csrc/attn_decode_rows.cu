@@ -349,8 +349,6 @@ __global__ void __launch_bounds__(RowCfg<D, NB, kQ8>::kThreads, 1)
     float fac0[NB], fac1[NB];  // scale * log2 e * 2^(row shift) of query rows 2t and 2t + 1
     ok = ok && ptx::mbar_wait_a(ptx::smem_u32(&q_bars[piece & 1]), (uint32_t)(piece >> 1) & 1u,
                                 abort_flag, p.err, kDevErrTimeoutProducer);
-    // lanes may give up apart from each other, and the votes below need them all
-    ok = __all_sync(0xffffffffu, ok);
     const uint4* q_s =
         reinterpret_cast<const uint4*>(smem + C::kOffQ + (piece & 1) * (C::kRows * D * 2));
     if constexpr (!kQ8) {
@@ -431,11 +429,13 @@ __global__ void __launch_bounds__(RowCfg<D, NB, kQ8>::kThreads, 1)
       m[nb][0] = m[nb][1] = R[nb][0] = R[nb][1] = kLowest;
       l[nb][0] = l[nb][1] = 0.0f;
     }
-    for (int k0 = w.t0 * 128 + warp * kUnit; k0 < key_end && ok; k0 += kWarps * kUnit) {
+    for (int k0 = w.t0 * 128 + warp * kUnit; k0 < key_end; k0 += kWarps * kUnit) {
       const int s = done % S;
       const int left = key_end - k0;  // visible keys of the block: [0, left)
-      ok = ptx::mbar_wait_a(ptx::smem_u32(&bars[s]), (uint32_t)(done / S) & 1u, abort_flag, p.err,
-                            kDevErrTimeoutProducer);
+      // lanes may give up a wait apart from each other (that for Q too), and the votes below
+      // need them all: only this one ends the loop
+      ok = ok && ptx::mbar_wait_a(ptx::smem_u32(&bars[s]), (uint32_t)(done / S) & 1u, abort_flag,
+                                  p.err, kDevErrTimeoutProducer);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       if (kQ8 && pending) store_exps(n_issued - 1, pend_ke, pend_ve);
