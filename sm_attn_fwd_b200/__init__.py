@@ -590,14 +590,29 @@ _ext = None
 def _native():
     """The native part of the binding (built first if it is absent and the compilers
     exist): the calls that a serving loop makes every step check their tensors, allocate
-    and call the library there, in a third to a half of the host time."""
+    and call the library there, in a third to a half of the host time.
+
+    An object built for another interpreter, torch or C ABI is not loaded.  Nor is the
+    library replaced once this process has it: the native part would load the new file
+    beside the old one, with a device error word of its own."""
     global _ext
     if _ext is None:
+        from . import build as _build
+        with _lock:
+            if _ext is None:
+                if not os.path.exists(_EXT_PATH):
+                    if _lib is not None and not _build.lib_is_current():
+                        raise RuntimeError(
+                            f"{_EXT_PATH} is missing and {_LIB_PATH}, which this process has "
+                            "loaded, is out of date: run python -m sm_attn_fwd_b200.build and "
+                            "start again")
+                    _build.build_ext()
+                elif not _build.is_current(_EXT_PATH):
+                    raise RuntimeError(
+                        f"{_EXT_PATH} was built for another Python, torch or attn.h: run "
+                        "python -m sm_attn_fwd_b200.build")
         load_library()
         with _lock:
-            if not os.path.exists(_EXT_PATH):
-                from . import build as _build
-                _build.build_ext()
             if _ext is None:
                 spec = importlib.util.spec_from_file_location("attn_torch", _EXT_PATH)
                 ext = importlib.util.module_from_spec(spec)

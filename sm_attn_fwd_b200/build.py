@@ -21,6 +21,7 @@ LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libattn_b200.so")
 EXT = os.path.join(LIBDIR, "attn_torch.so")
 EXT_SOURCE = "torch_binding.cpp"
+EXT_MARK = b"attn_torch built for "  # in the object, before its stamp
 SOURCES = ["attn_api.cu", "attn_kernels.cu", "attn_prefill.cu", "attn_short.cu", "attn_noalloc.cu",
            "attn_backward.cu", "attn_cache_q8.cu", "attn_decode_rows.cu",
            "attn_decode_q8_wide.cu", "attn_prefix.cu"]
@@ -72,10 +73,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(LIBDIR, exist_ok=True)
     stamp = os.path.join(LIBDIR, "libattn_b200.sha")
     digest = _digest()
-    if not force and os.path.exists(LIB) and os.path.exists(stamp):
-        with open(stamp) as f:
-            if f.read().strip() == digest:
-                return LIB
+    if not force and lib_is_current():
+        return LIB
     nvcc = nvcc_path()
     objs = []
     for src in SOURCES:
@@ -102,24 +101,44 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def _ext_stamp() -> str:
+    """What the native part of the binding is built for: this interpreter and torch (it uses
+    torch's C++ interface), its source and the C ABI it calls."""
+    import torch
+
+    h = hashlib.sha256(f"{sys.version} {torch.__version__}".encode())
+    for path in (os.path.join(CSRC, EXT_SOURCE), os.path.join(ROOT, "include", "attn.h")):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()[:16]
+
+
+def is_current(ext: str = EXT) -> bool:
+    """Whether the native part of the binding was built for this interpreter, torch and C
+    ABI (the object says so itself): another build's must not be loaded."""
+    with open(ext, "rb") as f:
+        return EXT_MARK + _ext_stamp().encode() in f.read()
+
+
+def lib_is_current() -> bool:
+    """Whether the library was built from these sources."""
+    stamp = os.path.join(LIBDIR, "libattn_b200.sha")
+    if not os.path.exists(LIB) or not os.path.exists(stamp):
+        return False
+    with open(stamp) as f:
+        return f.read().strip() == _digest()
+
+
 def build_ext(force: bool = False, verbose: bool = False) -> str:
     """Compile the native part of the binding if its sources, the interpreter or torch
-    changed (it uses torch's C++ interface); return its path."""
+    changed; return its path."""
     import sysconfig
 
     import torch
 
     lib = build(force, verbose)
-    h = hashlib.sha256(f"{sys.version} {torch.__version__}".encode())
-    for path in (os.path.join(CSRC, EXT_SOURCE), os.path.join(ROOT, "include", "attn.h")):
-        with open(path, "rb") as f:
-            h.update(f.read())
-    digest = h.hexdigest()[:16]
-    stamp = os.path.join(LIBDIR, "attn_torch.sha")
-    if not force and os.path.exists(EXT) and os.path.exists(stamp):
-        with open(stamp) as f:
-            if f.read().strip() == digest:
-                return EXT
+    if not force and os.path.exists(EXT) and is_current(EXT):
+        return EXT
     t = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
     includes = [os.path.join(t, "include"), os.path.join(cuda, "include"),
@@ -127,6 +146,7 @@ def build_ext(force: bool = False, verbose: bool = False) -> str:
     tmp = EXT + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f'-DATTN_TORCH_MARK="{EXT_MARK.decode() + _ext_stamp()}"',
            "-I", os.path.join(ROOT, "include")]
     for path in includes:
         cmd += ["-isystem", path]
@@ -138,8 +158,6 @@ def build_ext(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {EXT_SOURCE}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, EXT)
-    with open(stamp, "w") as f:
-        f.write(digest)
     return EXT
 
 

@@ -361,4 +361,8 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "attn_torch", nullptr, -1, g_meth
 
 }  // namespace
 
+// Which interpreter, torch and C ABI this object is built for; looked up before it is loaded.
+extern "C" __attribute__((used, visibility("default"))) const char attn_torch_mark[] =
+    ATTN_TORCH_MARK;
+
 PyMODINIT_FUNC PyInit_attn_torch() { return PyModule_Create(&g_module); }
