@@ -483,7 +483,7 @@ attn_status_t attn_decode_shared_prefix_paged(
  *   k_cache, v_cache, k_exp, v_exp  the cache above, written
  *   kv_lens  [B] int32 DEVICE array, each in [n_b, Lk_max]
  *   new_lens [B] int32 DEVICE array, each in [0, Ln], or NULL
- *   B, Hkv, Ln, Lk_max >= 1, B * Hkv * Ln < 2^31 - 4096 (else UNSUPPORTED); d in
+ *   B, Hkv, Ln, Lk_max >= 1, B * Hkv * Ln <= 2^31 - 65536 (else UNSUPPORTED); d in
  *   {64, 128}
  * A sequence whose kv_lens or new_lens entry is out of range is skipped and
  * flags the device error word (ATTN_ERR_INVALID_ARG).
@@ -519,7 +519,7 @@ attn_status_t attn_cache_append_paged_q8(const void* k, const void* v, void* k_p
  *   k, v     [B, Hkv, Lk_max, d] bf16, rows below kv_lens[b] written (the exact
  *            values code * 2^(e - 127), which bf16 holds in its normal range); the
  *            other rows are left as they were
- *   B * Hkv * Lk_max < 2^31 - 4096 (else UNSUPPORTED); the rest as for
+ *   B * Hkv * Lk_max <= 2^31 - 65536 (else UNSUPPORTED); the rest as for
  *   attn_cache_append_q8
  * Errors: INVALID_ARG / UNSUPPORTED before any launch; CUDA on launch failure.
  */

@@ -1433,8 +1433,10 @@ attn_status_t attn_decode_shared_prefix_paged(
 // ------------------------------------------------------- 8-bit KV cache
 namespace {
 
-// Rows of one call: row counters are 32-bit, with room for the last block's.
-constexpr long long kMaxCacheRows = 0x7fffffffLL - 4096;
+// Rows of one call: row counters are 32-bit, with room for the last block's, and so is
+// the number of a block's (sequence, head) pair, which the grid rounds up to a multiple of
+// 65535.
+constexpr long long kMaxCacheRows = 0x7fffffffLL - 65535;
 
 // Arguments shared by append and read-back.
 attn_status_t cache_params(const void* k_codes, const void* v_codes, const uint8_t* k_exp,
