@@ -38,9 +38,9 @@ template <int D>
 cudaError_t launch_short(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
                          const FwdParams&, int, cudaStream_t);
 template <int D>
-cudaError_t launch_cache_append(const CacheParams&, cudaStream_t);
+cudaError_t launch_cache_append(const CacheParams&, int num_sms, cudaStream_t);
 template <int D>
-cudaError_t launch_cache_read(const CacheParams&, cudaStream_t);
+cudaError_t launch_cache_read(const CacheParams&, int num_sms, cudaStream_t);
 template <int D, bool kQ8>
 cudaError_t launch_decode_rows(const CUtensorMap&, const CUtensorMap&, const DecodeParams&,
                                cudaStream_t);
@@ -1482,7 +1482,8 @@ attn_status_t append_impl(const void* k, const void* v, void* k_codes, void* v_c
   if (!p.err) return ATTN_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e =
-      d == 64 ? attn::launch_cache_append<64>(p, st) : attn::launch_cache_append<128>(p, st);
+      d == 64 ? attn::launch_cache_append<64>(p, num_sms(), st)
+              : attn::launch_cache_append<128>(p, num_sms(), st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -1501,7 +1502,8 @@ attn_status_t read_impl(const void* k_codes, const void* v_codes, const uint8_t*
   if (!p.err) return ATTN_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e =
-      d == 64 ? attn::launch_cache_read<64>(p, st) : attn::launch_cache_read<128>(p, st);
+      d == 64 ? attn::launch_cache_read<64>(p, num_sms(), st)
+              : attn::launch_cache_read<128>(p, num_sms(), st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -223,7 +223,9 @@ __global__ void __launch_bounds__(kCacheThreads) attn_cache_read_kernel(const Ca
 // limit, append of 7 x 4 heads, up to 2064: 5.7 / 5.3; one token for 64 x 8 heads:
 // 3.2 / 2.0; read-back of 5 x 4 heads, up to 2064: 4.5 / 3.9.
 constexpr int kRowsPerGroup = 4;
-bool many_rows(long long rows, int lanes) { return rows * lanes > 2LL * 148 * 2048; }
+bool many_rows(long long rows, int lanes, int num_sms) {
+  return rows * lanes > 2LL * num_sms * 2048;
+}
 
 // Chunks of `rows` rows by (b, h) pairs, the pairs in y and z (each at most 65535).
 dim3 cache_grid(int rows, int lanes, int u, long long pairs) {
@@ -236,10 +238,10 @@ dim3 cache_grid(int rows, int lanes, int u, long long pairs) {
 }  // namespace
 
 template <int D>
-cudaError_t launch_cache_append(const CacheParams& p, cudaStream_t stream) {
+cudaError_t launch_cache_append(const CacheParams& p, int num_sms, cudaStream_t stream) {
   constexpr int kLanes = D / 8, U = kRowsPerGroup;
   const long long pairs = (long long)p.B * p.Hkv;
-  if (many_rows(pairs * p.Ln, kLanes))
+  if (many_rows(pairs * p.Ln, kLanes, num_sms))
     attn_cache_append_kernel<D, U>
         <<<cache_grid(p.Ln, kLanes, U, pairs), kCacheThreads, 0, stream>>>(p);
   else
@@ -249,10 +251,10 @@ cudaError_t launch_cache_append(const CacheParams& p, cudaStream_t stream) {
 }
 
 template <int D>
-cudaError_t launch_cache_read(const CacheParams& p, cudaStream_t stream) {
+cudaError_t launch_cache_read(const CacheParams& p, int num_sms, cudaStream_t stream) {
   constexpr int kLanes = D / 8, U = kRowsPerGroup;
   const long long pairs = (long long)p.B * p.Hkv;
-  if (many_rows(pairs * p.Lk, kLanes))
+  if (many_rows(pairs * p.Lk, kLanes, num_sms))
     attn_cache_read_kernel<D, U>
         <<<cache_grid(p.Lk, kLanes, U, pairs), kCacheThreads, 0, stream>>>(p);
   else
@@ -261,9 +263,9 @@ cudaError_t launch_cache_read(const CacheParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template cudaError_t launch_cache_append<64>(const CacheParams&, cudaStream_t);
-template cudaError_t launch_cache_append<128>(const CacheParams&, cudaStream_t);
-template cudaError_t launch_cache_read<64>(const CacheParams&, cudaStream_t);
-template cudaError_t launch_cache_read<128>(const CacheParams&, cudaStream_t);
+template cudaError_t launch_cache_append<64>(const CacheParams&, int, cudaStream_t);
+template cudaError_t launch_cache_append<128>(const CacheParams&, int, cudaStream_t);
+template cudaError_t launch_cache_read<64>(const CacheParams&, int, cudaStream_t);
+template cudaError_t launch_cache_read<128>(const CacheParams&, int, cudaStream_t);
 
 }  // namespace attn

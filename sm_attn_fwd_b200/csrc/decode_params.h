@@ -26,8 +26,9 @@ struct CacheParams {
   int pages_per_seq, num_pages;
 };
 
-// Decode over an 8-bit cache, or a bf16 one with few query rows.  The work is shared among num_ctas CTAs as decode_sched.cuh
-// describes; CTA c's partial results are slots 2 c and 2 c + 1 of the workspace.
+// Decode over an 8-bit cache, or a bf16 one with few query rows.  The work is shared among
+// num_ctas CTAs as decode_sched.cuh describes; CTA c's partial results are slots 2 c and
+// 2 c + 1 of the workspace.
 struct DecodeParams {
   const void* q;  // bf16 [B, Hq, Lq, d]
   void* o;        // bf16 [B, Hq, Lq, d]
@@ -59,9 +60,12 @@ struct DecodeParams {
 
 // Cost, in key tiles, of starting on and finishing a unit (decode_sched.cuh).  A tile of
 // an 8-bit cache at d = 64 is half the bytes of any other, so it counts more of them:
-// 16 x 16 heads, 1 to 4099 keys, one row: 28.7 us with 5, 32.1 with 3; a bf16 cache
-// (24 x 4 heads, up to 2064 keys, 16 rows, behind a prefix of 8190): 26.8 us with 5,
-// 25.2 with 3.  At d = 128, 2 to 8 measure alike.
+// 16 x 16 heads, 1 to 4099 keys, one row: 27.6 us with 5, 29.7 with 3.  Elsewhere the two lie
+// within 5 % of each other, on either side.  With 3 and with 5, us, 32 x 8 heads, 1 to 2000
+// keys, 8-bit: d = 64, 16 rows 26.6, 25.8; 32 rows 42.0, 40.2; 128 rows 49.6, 51.7; d = 128,
+// 8 rows 26.4, 25.7; 16 rows 34.5, 34.8; 128 rows 66.0, 67.5.  bf16 behind a prefix of 512:
+// d = 64, 1 row 21.5, 21.3; 8 rows 24.0, 23.1; 32 rows 40.8, 38.9; d = 128, 1 row 35.4, 35.5;
+// 16 rows 39.4, 40.6.
 inline int piece_tiles(int d, bool q8, int tile_rows) {
   return q8 && d == 64 && tile_rows == 8 ? 5 : 3;
 }
@@ -69,8 +73,8 @@ inline int piece_tiles(int d, bool q8, int tile_rows) {
 // Query rows per unit for `rows` query rows per KV head.  Up to 16 (32 at d = 64) go
 // through mma.m16n8k16 (attn_decode_rows.cu), the smallest of its tiles that holds them;
 // for more, tcgen05 tiles of 128 rows are faster.  16 sequences x 8 KV heads x 16384
-// keys in 8 bits, 32 rows: 213 us through tcgen05 against 250 at d = 128, 179 against
-// 130 at d = 64; 16 rows: 110 and 80 us through m16n8k16.
+// keys in 8 bits, through m16n8k16 and through tcgen05, us: d = 128, 16 rows 112 and 196,
+// 17 to 32 rows 279 and 196; d = 64, 16 rows 81 and 170, 17 to 32 rows 128 and 170.
 inline int decode_tile_rows(int d, long long rows) {
   if (rows <= 8) return 8;
   if (rows <= 16) return 16;
