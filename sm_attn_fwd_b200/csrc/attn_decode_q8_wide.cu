@@ -41,7 +41,7 @@
 // 32 KB out to the expansion, 64 KB back and 96 KB to the MMAs, 1750 cycles at 128
 // bytes a cycle, against 1400 cycles that the codes take to arrive at the SM's share
 // of the copy bandwidth and 1024 each for the MMAs and the exponentials.  It takes about
-// 2900: a softmax's chain per tile (wait, load of S, maximum, exponentials, store of
+// 3000: a softmax's chain per tile (wait, load of S, maximum, exponentials, store of
 // P) and the expansion's share of the issue slots; with the expansion's arithmetic left
 // out it still takes 94 % of the time.  Measured: 16 x 8 KV heads x 16384 keys, 128 query
 // rows: 208 us (2.6 TB/s); up to 32768 keys in 16-key pages: 296 us, where bytes and

@@ -21,9 +21,9 @@
 // Measured: 64 sequences x 8 KV heads, 32768 keys of d = 128 in 8 bits at most (2.7 GB),
 // 8 query rows: 413 to 430 us, 6.3 to 6.5 TB/s, 96 to 99 % of the measured copy
 // bandwidth.  At d = 64 a key has half the bytes and as many instructions but for its
-// products: 16 x 16 heads x 16384 keys take 115 us, 4.7 TB/s, with 60 % of the issue
-// slots and 56 % of the integer pipe (conversions, permutes) in use.  16 x 16 heads
-// of up to 4099 keys: 28.7 us against 10.4 at the copy bandwidth, where the start, the
+// products: 16 x 16 heads x 16384 keys take 115 to 120 us, 4.5 to 4.7 TB/s, with 58 % of
+// the issue slots and 55 % of the integer pipe (conversions, permutes) in use.  16 x 16
+// heads of up to 4099 keys: 27 to 29 us against 10.4 at the copy bandwidth, where the start, the
 // pieces' ends and the merge kernel are about half of the time.
 //
 // Numbers, 8-bit cache.  Q is scaled per row by a power of two into f16's upper range
