@@ -101,23 +101,31 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
-def _ext_stamp() -> str:
+EXT_INPUTS = (os.path.join(CSRC, EXT_SOURCE), os.path.join(ROOT, "include", "attn.h"))
+
+
+def _ext_mark(parts: int = 2) -> bytes:
     """What the native part of the binding is built for: this interpreter and torch (it uses
-    torch's C++ interface), its source and the C ABI it calls."""
+    torch's C++ interface), then its source and the C ABI it calls."""
     import torch
 
-    h = hashlib.sha256(f"{sys.version} {torch.__version__}".encode())
-    for path in (os.path.join(CSRC, EXT_SOURCE), os.path.join(ROOT, "include", "attn.h")):
+    env = hashlib.sha256(f"{sys.version} {torch.__version__}".encode()).hexdigest()[:16]
+    if parts == 1:
+        return EXT_MARK + env.encode()
+    h = hashlib.sha256()
+    for path in EXT_INPUTS:
         with open(path, "rb") as f:
             h.update(f.read())
-    return h.hexdigest()[:16]
+    return EXT_MARK + f"{env} {h.hexdigest()[:16]}".encode()
 
 
 def is_current(ext: str = EXT) -> bool:
-    """Whether the native part of the binding was built for this interpreter, torch and C
-    ABI (the object says so itself): another build's must not be loaded."""
+    """Whether the native part of the binding was built for this interpreter and torch and,
+    where its sources are there to compare, from them (the object says so itself): another
+    build's must not be loaded."""
+    parts = 2 if all(os.path.exists(path) for path in EXT_INPUTS) else 1
     with open(ext, "rb") as f:
-        return EXT_MARK + _ext_stamp().encode() in f.read()
+        return _ext_mark(parts) in f.read()
 
 
 def lib_is_current() -> bool:
@@ -146,7 +154,7 @@ def build_ext(force: bool = False, verbose: bool = False) -> str:
     tmp = EXT + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
-           f'-DATTN_TORCH_MARK="{EXT_MARK.decode() + _ext_stamp()}"',
+           f'-DATTN_TORCH_MARK="{_ext_mark().decode()}"',
            "-I", os.path.join(ROOT, "include")]
     for path in includes:
         cmd += ["-isystem", path]

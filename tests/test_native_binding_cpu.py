@@ -34,14 +34,28 @@ def test_the_built_object_is_loaded_and_not_built_again(place):
     assert ab._native() is ab._native()
 
 
-def test_an_object_of_another_build_is_not_loaded(place):
-    path = place / "attn_torch.so"
+def other_build(path, part):
+    """The object with another digest for its environment (part 0) or its sources (1)."""
     data = path.read_bytes()
-    at = data.index(build.EXT_MARK) + len(build.EXT_MARK)
+    at = data.index(build.EXT_MARK) + len(build.EXT_MARK) + 17 * part
+    path.unlink()  # this process may have it mapped
     path.write_bytes(data[:at] + b"0123456789abcdef" + data[at + 16:])
+
+
+@pytest.mark.parametrize("part", [0, 1])
+def test_an_object_of_another_build_is_not_loaded(place, part):
+    other_build(place / "attn_torch.so", part)
     with pytest.raises(RuntimeError, match="sm_attn_fwd_b200.build"):
         ab._native()
     assert ab._ext is None
+
+
+def test_without_the_sources_only_the_environment_counts(place, monkeypatch):
+    monkeypatch.setattr(build, "EXT_INPUTS", (str(place / "missing.cpp"),))
+    other_build(place / "attn_torch.so", 1)
+    assert hasattr(ab._native(), "decode_q8")
+    other_build(place / "attn_torch.so", 0)
+    assert not build.is_current(build.EXT)
 
 
 def test_another_torch_makes_it_another_build(place, monkeypatch):
